@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libmxgemm.so")
 # C-ABI entry points declared in include/libmxgemm.h
 EXPORTS = ("mxgemm_status_string", "mxgemm_run", "mxgemm_run_noalloc", "mxgemm_run_bf16a", "mxgemm_pack_b", "mxgemm_pack_scales", "mxgemm_pack_a",
            "mxgemm_pack_a_bytes", "mxgemm_quantize",
-           "mxgemm_f16_run", "mxgemm_query", "mxgemm_plan", "mxgemm_query_ex", "mxgemm_plan_ex",
+           "mxgemm_f16_run", "mxgemm_route", "mxgemm_route_workspace_bytes", "mxgemm_grouped_run", "mxgemm_glu_quantize",
+           "mxgemm_norm_quantize", "mxgemm_query", "mxgemm_plan", "mxgemm_query_ex", "mxgemm_plan_ex",
            "mxgemm_stream_read", "mxgemm_release_workspaces")
 
 STATUS = {0: "MXGEMM_OK", -1: "MXGEMM_ERR_INVALID_ARG", -2: "MXGEMM_ERR_SHAPE",
@@ -70,6 +71,22 @@ class Info(ctypes.Structure):
         return d
 
 
+class Grouped(ctypes.Structure):
+    _fields_ = [("ldd", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldsb", ctypes.c_int64), ("strideb", ctypes.c_int64), ("strideb_scale", ctypes.c_int64),
+                ("a_format", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("pos", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("top_k", ctypes.c_int32), ("y_rows", ctypes.c_int32), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float), ("H", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("w_pre", ctypes.c_void_p), ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("A", ctypes.c_void_p),
+                ("scaleA", ctypes.c_void_p), ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64),
+                ("a_format", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -103,6 +120,17 @@ def lib():
         L.mxgemm_quantize.restype = i32
         L.mxgemm_f16_run.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i64, vp]
         L.mxgemm_f16_run.restype = i32
+        L.mxgemm_route.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i32, vp, ctypes.c_size_t, vp]
+        L.mxgemm_route.restype = i32
+        L.mxgemm_route_workspace_bytes.argtypes = [i32, i32]
+        L.mxgemm_route_workspace_bytes.restype = ctypes.c_size_t
+        L.mxgemm_grouped_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, i32, i32, i32, i32,
+                                         ctypes.POINTER(Grouped), vp]
+        L.mxgemm_grouped_run.restype = i32
+        L.mxgemm_glu_quantize.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i64, i32, vp]
+        L.mxgemm_glu_quantize.restype = i32
+        L.mxgemm_norm_quantize.argtypes = [ctypes.POINTER(Norm), i32, i32, vp]
+        L.mxgemm_norm_quantize.restype = i32
         L.mxgemm_query.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
         L.mxgemm_query.restype = i32
         L.mxgemm_plan.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
@@ -255,6 +283,68 @@ def mxgemm_f16_run(C, A, B, M, N, K, lda=None, ldb=None, ldc=None, stream=None, 
                               _stream(stream))
     if check:
         _check(st, "mxgemm_f16_run")
+    return st
+
+
+def mxgemm_route(ids, weights, pos, offsets, rows, logits, T, E, top_k, ldl=None, bf16=False, renorm=True,
+                 workspace=None, workspace_bytes=0, stream=None, check=True):
+    """Router logits -> each token's top_k experts and weights, and the rows
+    ordered by expert (asynchronous; workspace: mxgemm_route_workspace_bytes)."""
+    st = lib().mxgemm_route(_ptr(ids), _ptr(weights), _ptr(pos), _ptr(offsets), _ptr(rows), _ptr(logits), int(bf16),
+                            int(T), int(E), int(top_k), int(E if ldl is None else ldl), int(renorm), _ptr(workspace),
+                            int(workspace_bytes), _stream(stream))
+    if check:
+        _check(st, "mxgemm_route")
+    return st
+
+
+def mxgemm_route_workspace_bytes(T, E) -> int:
+    return int(lib().mxgemm_route_workspace_bytes(int(T), int(E)))
+
+
+def mxgemm_grouped_run(D, A, B, scaleA, scaleB, offsets, rows, N, K, groups, a_rows=None, a_count=None, alpha=1.0,
+                       a_format=FMT_FP4, ldd=None, lda=None, ldsa=None, ldb=None, ldsb=None, strideb=None,
+                       strideb_scale=None, stream=None, check=True):
+    """D[i] = bf16(alpha * A[a_rows[i]] * B[e]^T) for the rows i of each
+    expert e (offsets; asynchronous; strides default to dense)."""
+    KB = K // 32
+    ldb = K if ldb is None else ldb
+    ldsb = KB if ldsb is None else ldsb
+    g = Grouped(N if ldd is None else ldd, K if lda is None else lda, KB if ldsa is None else ldsa, ldb, ldsb,
+                N * ldb if strideb is None else strideb, N * ldsb if strideb_scale is None else strideb_scale, a_format)
+    st = lib().mxgemm_grouped_run(_ptr(D), _ptr(A), _ptr(B), _ptr(scaleA), _ptr(scaleB), _ptr(offsets), _ptr(a_rows),
+                                  float(alpha), int(rows), int(rows if a_count is None else a_count), int(N), int(K),
+                                  int(groups), ctypes.byref(g), _stream(stream))
+    if check:
+        _check(st, "mxgemm_grouped_run")
+    return st
+
+
+def mxgemm_glu_quantize(A, scaleA, X, M, K, live=None, ldx=None, lda=None, ldsa=None, a_format=FMT_FP4, stream=None,
+                        check=True):
+    """bf16 X [M][gate K | up K] -> quantized silu(gate) * up (asynchronous;
+    rows from *live on are left; strides default to dense rows)."""
+    st = lib().mxgemm_glu_quantize(_ptr(A), _ptr(scaleA), _ptr(X), _ptr(live), int(M), int(K),
+                                   int(2 * K if ldx is None else ldx), int(K if lda is None else lda),
+                                   int(K // 32 if ldsa is None else ldsa), int(a_format), _stream(stream))
+    if check:
+        _check(st, "mxgemm_glu_quantize")
+    return st
+
+
+def mxgemm_norm_quantize(T, K, Y, X=None, H=None, Z=None, A=None, scaleA=None, pos=None, weights=None, top_k=0, y_rows=0,
+                         w_post=None, gate=None, res_scale=1.0, w_pre=None, eps=1e-6, a_format=FMT_FP4, ldy=None,
+                         ldg=None, ldx=None, ldh=None, ldz=None, lda=None, ldsa=None, stream=None, check=True):
+    """Weighted sum of a token's rows of Y, norm, gate, residual -> H; its
+    norm -> Z and, quantized, A and scaleA (asynchronous; strides default to
+    dense rows; a gate of one row for all tokens: ldg=0)."""
+    ld = [K if v is None else v for v in (ldy, ldg, ldx, ldh, ldz, lda)]
+    n = Norm(_ptr(Y), ld[0], _ptr(pos), _ptr(weights), top_k, y_rows, _ptr(w_post), _ptr(gate), ld[1], _ptr(X), ld[2],
+             res_scale, eps, _ptr(H), ld[3], _ptr(w_pre), _ptr(Z), ld[4], _ptr(A), _ptr(scaleA), ld[5],
+             K // 32 if ldsa is None else ldsa, a_format)
+    st = lib().mxgemm_norm_quantize(ctypes.byref(n), int(T), int(K), _stream(stream))
+    if check:
+        _check(st, "mxgemm_norm_quantize")
     return st
 
 

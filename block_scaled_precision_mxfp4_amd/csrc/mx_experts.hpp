@@ -1,0 +1,77 @@
+// Arguments and launchers of the mixture-of-experts kernels (router choice,
+// product grouped by expert, gated activation with quantizer, norms with
+// residual and quantizer).  Host-side only plain types; no device code.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mx {
+
+// ---- router choice (mx_route.hip)
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopK = 16;
+constexpr int kRouteUnit = 64;        // tokens whose slots are ranked together
+constexpr int kRouteMaxBlocks = 256;  // workgroups of the selection; each takes whole units
+struct RouteArgs {
+    const void *logits;  // f32 or bf16 [T][ldl]
+    int32_t *ids;        // [T][k]
+    float *weights;      // [T][k]
+    int32_t *pos;        // [T][k]
+    int32_t *offsets;    // [E + 1]
+    int32_t *rows;       // [T * k]
+    int32_t *counts;     // workspace [blocks][E] (blocks > 1)
+    int T, E, k;
+    int64_t ldl;
+    int bf16, renorm;
+    int units;           // 64-token units per workgroup
+    int blocks;
+};
+void launch_route(const RouteArgs &r, hipStream_t s);
+
+// ---- gated activation and quantizer (mx_glu.hip)
+struct GluArgs {
+    const uint16_t *X;    // bf16 [M][ldx]: gate columns 0..K-1, up columns K..2K-1
+    const int32_t *live;  // device count of rows to do, or null
+    uint8_t *A, *S;
+    int M, K;
+    int64_t ldx, lda_b, lds;
+    int64_t blocks;       // M * K / 32
+    int fp8;
+};
+int64_t glu_grid(int64_t blocks);
+void launch_glu(const GluArgs &g, hipStream_t s);
+
+// ---- norms around a block (mx_norm.hip)
+constexpr int kNormMaxK = 16384;
+struct NormArgs {
+    const uint16_t *Y;       // block output, bf16 [y_rows][ldy]
+    const int32_t *pos;      // [T][top_k] rows of Y, or null (row t)
+    const float *weights;    // [T][top_k]
+    const uint16_t *w_post, *gate, *X, *w_pre;  // each may be null
+    uint16_t *H, *Z;         // may be null
+    uint8_t *A, *S;          // may be null (both)
+    int T, K, top_k, y_rows;
+    int64_t ldy, ldg, ldx, ldh, ldz, lda_b, lds;
+    float res_scale, eps;
+    int fp8;
+};
+void launch_norm(const NormArgs &n, hipStream_t s);
+
+// ---- product grouped by expert (mx_grouped.hip)
+struct GroupedArgs {
+    uint16_t *D;             // bf16 [rows][ldd]
+    const uint8_t *A, *B, *SA, *SB;
+    const int32_t *offsets;  // [E + 1]
+    const int32_t *a_rows;   // [rows] or null
+    float alpha;
+    int rows, a_count, N, K, KB, E;
+    int64_t ldd, lda_b, ldsa, ldb_b, ldsb, eb_b, esb;  // bytes (ldd: elements); eb_b, esb: expert to expert
+    int d_vec, d_stage;      // 8-byte D stores; 16-byte D rows
+    int sa16, sb16;          // scale rows in 16-byte aligned groups of 16 K-blocks
+    int fp8;
+};
+void launch_grouped_stream(const GroupedArgs &g, hipStream_t s);
+
+}  // namespace mx

@@ -1,0 +1,184 @@
+// The norms around a block on gfx950, one workgroup per token, one pass over
+// memory:
+//   y = sum_j weight_j * Y[pos_j]            (the experts' rows, or row t of Y)
+//   n = y * rsqrt(mean(y^2) + eps) * w_post  (or y)
+//   h = bf16(x + res_scale * gate * n)
+//   z = bf16(h * rsqrt(mean(h^2) + eps) * w_pre)  (or h)
+// and z's 32-blocks in MXFP4 or MXFP8 (the next product's A).
+//
+// A thread keeps its 8 C elements of the token in registers from the first
+// load to the last store; the two means are sums over the workgroup.  All
+// arithmetic between the bf16 inputs and the bf16 results is in 64 bits
+// (products of bf16 values are exact there, and the multiply-add runs at
+// fp32's rate on this chip): h and z are the correctly rounded values up to
+// 2^-45 or so, whatever the order of the sums, so codes and scales do not
+// flip with it.
+//
+// Bound by HBM: 2 (top_k + 1) bytes read and 4 + 17/32 (FP4) or 33/32 (FP8)
+// written per element with every output asked for.
+#include "mx_device.hpp"
+#include "mx_experts.hpp"
+#include "mx_quantize.hpp"
+
+namespace mx {
+
+__device__ __forceinline__ double bf16_at(v4i x, int i)
+{
+    return (double)bf16_to_f32(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+}
+
+// Sum over the workgroup, the same bits in every thread; s: NW doubles of its
+// own (two sums in a row use different ones).
+template <int NW>
+__device__ __forceinline__ double block_sum(double v, double *s)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2)
+        v += __shfl_xor(v, d);
+    if constexpr (NW == 1)
+        return v;
+    if ((threadIdx.x & 63) == 0)
+        s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        t += s[w];
+    return t;
+}
+
+template <int NT, int C, bool FP8>
+__global__ void __launch_bounds__(NT) mx_norm_kernel(NormArgs a)
+{
+    __shared__ double s_sum[2][NT / 64];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x;
+    const v4i zero = {0, 0, 0, 0};
+    int e[C];
+    bool on[C];
+    v4i x[C], gate[C], wpost[C], wpre[C];
+    double y[C][8];
+    auto load = [&](const uint16_t *p, int c) __attribute__((always_inline)) {
+        return on[c] && p ? *reinterpret_cast<const v4i *>(p + e[c]) : zero;
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        e[c] = (c * NT + tid) * 8;
+        on[c] = e[c] < a.K;
+        x[c] = load(a.X ? a.X + t * a.ldx : nullptr, c);
+        gate[c] = load(a.gate ? a.gate + t * a.ldg : nullptr, c);
+        wpost[c] = load(a.w_post, c);
+        wpre[c] = load(a.w_pre, c);
+    }
+    if (a.pos) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[c][i] = 0.0;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int p = a.pos[t * a.top_k + j];
+            if (p < 0 || p >= a.y_rows)  // not routed (or no row of Y)
+                continue;
+            const double w = (double)a.weights[t * a.top_k + j];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const v4i r = load(a.Y + (int64_t)p * a.ldy, c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[c][i] = fma(w, bf16_at(r, i), y[c][i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const v4i r = load(a.Y + t * a.ldy, c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[c][i] = bf16_at(r, i);
+        }
+    }
+    if (a.w_post) {
+        double q = 0.0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q = fma(y[c][i], y[c][i], q);
+        const double inv = 1.0 / sqrt(block_sum<NT / 64>(q, s_sum[0]) / a.K + (double)a.eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[c][i] *= inv * bf16_at(wpost[c], i);
+    }
+    const double scale = (double)a.res_scale;
+    double q = 0.0;
+    v4i h[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float f[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int i = 2 * w + b;
+                double n = y[c][i];
+                if (a.gate)
+                    n *= bf16_at(gate[c], i);
+                f[b] = f32_for_bf16(fma(scale, n, bf16_at(x[c], i)));
+            }
+            h[c][w] = (int)bf16x2_rne(f[0], f[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q = fma(bf16_at(h[c], i), bf16_at(h[c], i), q);
+        if (a.H && on[c])
+            *reinterpret_cast<v4i *>(a.H + t * a.ldh + e[c]) = h[c];
+    }
+    if (!a.Z && !a.A)
+        return;
+    if (a.w_pre) {
+        const double inv = 1.0 / sqrt(block_sum<NT / 64>(q, s_sum[1]) / a.K + (double)a.eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float lo = f32_for_bf16(bf16_at(h[c], 2 * w) * inv * bf16_at(wpre[c], 2 * w));
+                const float hi = f32_for_bf16(bf16_at(h[c], 2 * w + 1) * inv * bf16_at(wpre[c], 2 * w + 1));
+                h[c][w] = (int)bf16x2_rne(lo, hi);
+            }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (a.Z && on[c])
+            *reinterpret_cast<v4i *>(a.Z + t * a.ldz + e[c]) = h[c];
+        if (a.A)
+            quantize_store<FP8>(h[c], a.A + t * a.lda_b, a.S + t * a.lds, e[c], on[c]);
+    }
+}
+
+template <int NT, int C>
+static void launch_norm_as(const NormArgs &n, hipStream_t s)
+{
+    if (n.fp8)
+        hipLaunchKernelGGL((mx_norm_kernel<NT, C, true>), dim3((unsigned)n.T), dim3(NT), 0, s, n);
+    else
+        hipLaunchKernelGGL((mx_norm_kernel<NT, C, false>), dim3((unsigned)n.T), dim3(NT), 0, s, n);
+}
+
+void launch_norm(const NormArgs &n, hipStream_t s)
+{
+    if (n.K <= 512)
+        launch_norm_as<64, 1>(n, s);
+    else if (n.K <= 2048)
+        launch_norm_as<256, 1>(n, s);
+    else if (n.K <= 4096)
+        launch_norm_as<256, 2>(n, s);
+    else if (n.K <= 8192)
+        launch_norm_as<512, 2>(n, s);
+    else
+        launch_norm_as<1024, 2>(n, s);
+}
+
+}  // namespace mx

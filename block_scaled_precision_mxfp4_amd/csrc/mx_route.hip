@@ -1,0 +1,339 @@
+// The router's choice on gfx950: from logits [T][E] each token's top k
+// experts with softmax weights, and the row list that orders the T*k chosen
+// (token, slot) pairs by expert for the grouped product.
+//
+// Selection.  16 lanes share a token, four tokens a wave; lane l keeps the
+// experts l, l + 16, ... as unsigned keys that order like the values (-inf
+// and NaN: key 0, never chosen; -0 is +0 first, so that equal values tie).
+// Each of the k rounds takes the largest key, then the lowest expert that has
+// it: two butterfly reductions over the 16 lanes with row permutes (no LDS).
+// Weights are exp(x - max) / sum in fp32, the sum over the chosen experts or
+// over all of them.
+//
+// Grouping, without atomics, so that the order is that of the tokens.  64
+// tokens' slots are ranked together: for 64 consecutive slots a wave finds
+// the lanes with the same expert from one ballot per bit of the expert's
+// number; the rank inside the wave is a population count, and a count per
+// (wave, expert) in LDS, summed over the waves in order, makes it the rank
+// inside the 64 tokens.  With one workgroup (T <= 64) the offsets follow in
+// the same launch; otherwise every workgroup leaves its counts in the
+// workspace and a second kernel adds the counts of the workgroups before it.
+//
+// Bound by latency (and for long inputs by reading the logits).
+#include "mx_device.hpp"
+#include "mx_experts.hpp"
+
+namespace mx {
+
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v, int step)
+{
+    // partner of step 0..3 inside 16 lanes: lane ^ 1, lane ^ 2, the mirrored
+    // lane of 8 and of 16 (whose quads and halves already agree)
+    switch (step) {
+    case 0: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+    case 1: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
+    case 2: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);
+    default: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);
+    }
+}
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v = max(v, dpp_u32(v, i));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t row_min(uint32_t v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v = min(v, dpp_u32(v, i));
+    return v;
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v += __uint_as_float(dpp_u32(__float_as_uint(v), i));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    if (!(x > -INFINITY))  // -inf or NaN
+        return 0;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// exp(x - m), 1 where x is the maximum itself (also a maximum of +inf)
+__device__ __forceinline__ float share(float x, float m) { return x == m ? 1.0f : expf(x - m); }
+
+// start[e] = sum of count[0 .. e-1], start[E] the total; by one wave
+__device__ __forceinline__ void exclusive_scan(const int *count, int *start, int E, int lane)
+{
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        const int c = e < E ? count[e] : 0;
+        int s = c;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(s, d);
+            s += lane >= d ? o : 0;
+        }
+        if (e < E)
+            start[e] = carry + s - c;
+        carry += __shfl(s, 63);
+    }
+    if (lane == 0)
+        start[E] = carry;
+}
+
+// V: experts per lane (E <= 16 V); NT: threads (16 NT-lane tokens a pass)
+template <int V, int NT, bool BF16>
+__global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
+{
+    constexpr int NW = NT / 64;
+    constexpr int TPP = NT / 16;                     // tokens per pass
+    constexpr int CPW = kRouteMaxTopK / NW > 0 ? kRouteMaxTopK / NW : 1;  // 64-slot chunks per wave
+    extern __shared__ int s_mem[];
+    int *s_base = s_mem;                             // [E + 1] rows of this workgroup per expert so far
+    int *s_start = s_mem + r.E + 1;                  // [E + 1]
+    int16_t *s_id = reinterpret_cast<int16_t *>(s_start + r.E + 1);  // [64 k]
+    uint16_t *s_cnt = reinterpret_cast<uint16_t *>(s_id + kRouteUnit * kRouteMaxTopK);  // [k][E]
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int l = lane & 15;
+    const int k = r.k, E = r.E;
+    for (int e = tid; e < E; e += NT)
+        s_base[e] = 0;
+
+    for (int unit = 0; unit < r.units; ++unit) {
+        const int64_t t0 = ((int64_t)blockIdx.x * r.units + unit) * kRouteUnit;
+        if (t0 >= r.T)
+            break;
+        for (int i = tid; i < k * E; i += NT)
+            s_cnt[i] = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < kRouteUnit / TPP; ++pass) {
+            const int u = pass * TPP + tid / 16;  // token of the unit
+            const int64_t t = t0 + u;
+            const bool live = t < r.T;
+            uint32_t key[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = v * 16 + l;
+                float x = -INFINITY;
+                if (live && e < E) {
+                    if constexpr (BF16)
+                        x = bf16_to_f32(reinterpret_cast<const uint16_t *>(r.logits)[t * r.ldl + e]);
+                    else
+                        x = reinterpret_cast<const float *>(r.logits)[t * r.ldl + e];
+                }
+                key[v] = key_of(x);
+            }
+            uint32_t best = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                best = max(best, key[v]);
+            best = row_max(best);
+            const float m = value_of(best);
+            float total = 0.0f;
+            if (!r.renorm) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    total += key[v] ? share(value_of(key[v]), m) : 0.0f;
+                total = row_sum(total);
+            }
+            int mine = -1;        // lane j keeps the j-th choice
+            uint32_t mine_key = 0;
+            for (int j = 0; j < k; ++j) {
+                uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+                for (int v = V - 1; v >= 0; --v)
+                    at = key[v] == best ? (uint32_t)(v * 16 + l) : at;
+                at = row_min(at);
+                if (l == j && best) {
+                    mine = (int)at;
+                    mine_key = best;
+                }
+                uint32_t next = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    key[v] = (uint32_t)(v * 16 + l) == at ? 0 : key[v];
+                    next = max(next, key[v]);
+                }
+                best = row_max(next);
+            }
+            const float p = mine >= 0 ? share(value_of(mine_key), m) : 0.0f;
+            if (r.renorm)
+                total = row_sum(p);
+            if (l < k) {
+                s_id[u * k + l] = (int16_t)mine;
+                if (live) {
+                    r.ids[t * k + l] = mine;
+                    r.weights[t * k + l] = mine >= 0 ? p / total : 0.0f;
+                }
+            }
+        }
+        __syncthreads();
+        // ranks: chunk c = 64 consecutive slots, by wave c % NW
+        int rank[CPW], id[CPW];
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) {
+            const int c = i * NW + wave;
+            rank[i] = 0;
+            id[i] = -1;
+            if (c < k) {
+                id[i] = s_id[c * 64 + lane];
+                uint64_t same = __ballot(id[i] >= 0);
+                for (int b = 0; (1 << b) < E; ++b) {
+                    const bool bit = (id[i] >> b) & 1;
+                    const uint64_t ones = __ballot(bit);
+                    same &= bit ? ones : ~ones;
+                }
+                const uint64_t before = same & ((1ull << lane) - 1);
+                rank[i] = __popcll(before);
+                if (id[i] >= 0 && before == 0)
+                    s_cnt[c * E + id[i]] = (uint16_t)__popcll(same);
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < E; e += NT) {
+            int run = 0;
+            for (int c = 0; c < k; ++c) {
+                const int n = s_cnt[c * E + e];
+                s_cnt[c * E + e] = (uint16_t)run;
+                run += n;
+            }
+            s_start[e] = run;  // this unit's rows of expert e
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) {
+            const int c = i * NW + wave;
+            const int64_t slot = t0 * k + c * 64 + lane;
+            if (c < k && slot < (int64_t)r.T * k)
+                r.pos[slot] = id[i] >= 0 ? s_base[id[i]] + s_cnt[c * E + id[i]] + rank[i] : -1;
+        }
+        __syncthreads();
+        for (int e = tid; e < E; e += NT)
+            s_base[e] += s_start[e];
+        __syncthreads();
+    }
+
+    if (r.blocks > 1) {
+        for (int e = tid; e < E; e += NT)
+            r.counts[(int64_t)blockIdx.x * E + e] = s_base[e];
+        return;
+    }
+    // one workgroup, one unit: the ranks are final, the offsets follow
+    if (wave == 0)
+        exclusive_scan(s_base, s_start, E, lane);
+    __syncthreads();
+    for (int e = tid; e <= E; e += NT)
+        r.offsets[e] = s_start[e];
+    const int n = r.T * k;
+    for (int i = tid; i < n; i += NT) {
+        if (i >= s_start[E])
+            r.rows[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < CPW; ++i) {
+        const int c = i * NW + wave;
+        const int slot = c * 64 + lane;
+        if (c < k && slot < n) {
+            const int e = s_id[slot];
+            if (e >= 0) {
+                const int p = s_start[e] + r.pos[slot];  // written by this thread above
+                r.pos[slot] = p;
+                r.rows[p] = slot / k;
+            }
+        }
+    }
+}
+
+// Second launch: workgroup b's ranks become positions.
+__global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
+{
+    extern __shared__ int s_mem[];
+    const int E = r.E, k = r.k;
+    int *s_total = s_mem, *s_before = s_mem + E, *s_start = s_mem + 2 * E;  // [E], [E], [E + 1]
+    const int tid = threadIdx.x;
+    for (int e = tid; e < E; e += 1024)
+        s_total[e] = s_before[e] = 0;
+    __syncthreads();
+    // 1024 / ep workgroups' counts at a time (E <= 1024); integer sums
+    int ep = 1;
+    while (ep < E)
+        ep *= 2;
+    const int e = tid & (ep - 1);
+    if (e < E) {
+        int total = 0, before = 0;
+        for (int b = tid / ep; b < r.blocks; b += 1024 / ep) {
+            const int c = r.counts[(int64_t)b * E + e];
+            total += c;
+            before += b < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(&s_total[e], total);
+        atomicAdd(&s_before[e], before);
+    }
+    __syncthreads();
+    if (tid < 64)
+        exclusive_scan(s_total, s_start, E, tid);
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= E; i += 1024)
+            r.offsets[i] = s_start[i];
+    const int64_t slots = (int64_t)r.T * k;
+    const int64_t first = (int64_t)blockIdx.x * r.units * kRouteUnit * k;
+    const int64_t last = min(slots, first + (int64_t)r.units * kRouteUnit * k);
+    for (int64_t i = first + tid; i < last; i += 1024) {
+        const int id = r.ids[i];
+        if (id >= 0) {
+            const int p = s_start[id] + s_before[id] + r.pos[i];
+            r.pos[i] = p;
+            r.rows[p] = (int32_t)(i / k);
+        }
+        if (i >= s_start[E])
+            r.rows[i] = -1;
+    }
+}
+
+template <int V, int NT>
+static void launch_select(const RouteArgs &r, hipStream_t s)
+{
+    const size_t lds = (size_t)(2 * (r.E + 1)) * 4 + kRouteUnit * kRouteMaxTopK * 2 + (size_t)r.k * r.E * 2;
+    if (r.bf16)
+        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, true>), dim3(r.blocks), dim3(NT), lds, s, r);
+    else
+        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, false>), dim3(r.blocks), dim3(NT), lds, s, r);
+}
+
+void launch_route(const RouteArgs &r, hipStream_t s)
+{
+    // 64 tokens a pass where a lane's keys leave room for 16 waves
+    if (r.E <= 32)
+        launch_select<2, 1024>(r, s);
+    else if (r.E <= 64)
+        launch_select<4, 1024>(r, s);
+    else if (r.E <= 128)
+        launch_select<8, 1024>(r, s);
+    else if (r.E <= 256)
+        launch_select<16, 1024>(r, s);
+    else
+        launch_select<64, 256>(r, s);
+    if (r.blocks > 1)
+        hipLaunchKernelGGL(mx_route_place_kernel, dim3(r.blocks), dim3(1024), (size_t)(3 * r.E + 1) * 4, s, r);
+}
+
+}  // namespace mx

@@ -22,6 +22,7 @@
 #include <utility>
 
 #include "mx_args.hpp"
+#include "mx_host.hpp"
 
 namespace mx {
 // GEMV (mx_gemv.hip): M == 1 with A in format a_fmt (0 FP4, 1..4 FP8 E4M3,
@@ -555,6 +556,15 @@ mxgemm_status check_shape(int M, int N, int K)
 bool valid_split(int s) { return s == 0 || s == -1 || s == 1 || s == 2 || s == 4 || s == 8 || s == 16; }
 
 }  // namespace
+
+mxgemm_status mx::check_device(int *num_cu)
+{
+    DeviceInfo *d = nullptr;
+    const mxgemm_status st = device_info(&d);
+    if (st == MXGEMM_OK && num_cu)
+        *num_cu = d->num_cu;
+    return st;
+}
 
 extern "C" {
 

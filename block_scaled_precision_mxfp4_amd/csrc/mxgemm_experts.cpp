@@ -1,0 +1,253 @@
+// C-ABI entry points of the mixture-of-experts operators declared in
+// libmxgemm.h: argument validation on the host, then one or two launches on
+// the caller's stream.  Nothing here allocates or keeps state.
+#include "libmxgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "mx_args.hpp"
+#include "mx_experts.hpp"
+#include "mx_host.hpp"
+
+namespace {
+
+constexpr int kMaxK = 1 << 24;
+constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// width in bits of the formats an operator here takes (0: not one of them)
+int elem_bits(int a_format)
+{
+    return a_format == MXGEMM_FMT_FP4 ? 4 : a_format == MXGEMM_FMT_FP8_E4M3 ? 8 : 0;
+}
+
+// A quantized output (rows of lda elements): extents, then alignment
+mxgemm_status check_quantized(const void *A, int K, int64_t lda, int64_t ldsa, int bits)
+{
+    if (lda < K || ldsa < K / 32)
+        return MXGEMM_ERR_SHAPE;
+    if (!aligned(A, 16) || (lda * bits) % 128)
+        return MXGEMM_ERR_ALIGN;
+    return MXGEMM_OK;
+}
+
+mxgemm_status launched() { return hipGetLastError() == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP; }
+
+int route_units(int T) { return (int)(((int64_t)T + mx::kRouteUnit - 1) / mx::kRouteUnit); }
+int route_units_per_block(int T) { return (route_units(T) + mx::kRouteMaxBlocks - 1) / mx::kRouteMaxBlocks; }
+int route_blocks(int T)
+{
+    const int per = route_units_per_block(T);
+    return (route_units(T) + per - 1) / per;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mxgemm_route_workspace_bytes(int T, int E)
+{
+    if (T < 1 || E < 1 || E > mx::kRouteMaxExperts)
+        return 0;
+    const int blocks = route_blocks(T);
+    return blocks > 1 ? (size_t)blocks * E * 4 : 0;
+}
+
+mxgemm_status mxgemm_route(int32_t *ids, float *weights, int32_t *pos, int32_t *offsets, int32_t *rows,
+                           const void *logits, int bf16, int T, int E, int top_k, int64_t ldl, int renorm,
+                           void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!ids || !weights || !pos || !offsets || !rows || !logits || (bf16 != 0 && bf16 != 1) ||
+        (renorm != 0 && renorm != 1))
+        return MXGEMM_ERR_INVALID_ARG;
+    if (T < 1 || E < 1 || E > mx::kRouteMaxExperts || top_k < 1 || top_k > mx::kRouteMaxTopK || top_k > E || ldl < E ||
+        (int64_t)T * top_k > kMaxGrid)
+        return MXGEMM_ERR_SHAPE;
+    if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(pos, 4) || !aligned(offsets, 4) || !aligned(rows, 4) ||
+        !aligned(logits, bf16 ? 2 : 4))
+        return MXGEMM_ERR_ALIGN;
+    const size_t need = mxgemm_route_workspace_bytes(T, E);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return MXGEMM_ERR_WORKSPACE;
+        if (!aligned(workspace, 4))
+            return MXGEMM_ERR_ALIGN;
+    }
+    mxgemm_status st = mx::check_device();
+    if (st != MXGEMM_OK)
+        return st;
+    mx::RouteArgs r;
+    r.logits = logits;
+    r.ids = ids;
+    r.weights = weights;
+    r.pos = pos;
+    r.offsets = offsets;
+    r.rows = rows;
+    r.counts = (int32_t *)workspace;
+    r.T = T;
+    r.E = E;
+    r.k = top_k;
+    r.ldl = ldl;
+    r.bf16 = bf16;
+    r.renorm = renorm;
+    r.units = route_units_per_block(T);
+    r.blocks = route_blocks(T);
+    mx::launch_route(r, stream);
+    return launched();
+}
+
+mxgemm_status mxgemm_glu_quantize(void *A, void *scaleA, const void *X, const int32_t *live, int M, int K, int64_t ldx,
+                                  int64_t lda, int64_t ldsa, int a_format, hipStream_t stream)
+{
+    const int bits = elem_bits(a_format);
+    if (!A || !scaleA || !X || !bits)
+        return MXGEMM_ERR_INVALID_ARG;
+    if (M < 1 || K < 32 || K % 32 || K > kMaxK || ldx < 2 * (int64_t)K)
+        return MXGEMM_ERR_SHAPE;
+    mxgemm_status st = check_quantized(A, K, lda, ldsa, bits);
+    if (st != MXGEMM_OK)
+        return st;
+    if (!aligned(X, 16) || ldx % 8 || !aligned(live, 4))
+        return MXGEMM_ERR_ALIGN;
+    const int64_t blocks = (int64_t)M * (K / 32);
+    if (mx::glu_grid(blocks) > kMaxGrid)
+        return MXGEMM_ERR_SHAPE;
+    st = mx::check_device();
+    if (st != MXGEMM_OK)
+        return st;
+    mx::GluArgs q;
+    q.X = (const uint16_t *)X;
+    q.live = live;
+    q.A = (uint8_t *)A;
+    q.S = (uint8_t *)scaleA;
+    q.M = M;
+    q.K = K;
+    q.ldx = ldx;
+    q.lda_b = lda * bits / 8;
+    q.lds = ldsa;
+    q.blocks = blocks;
+    q.fp8 = bits == 8;
+    mx::launch_glu(q, stream);
+    return launched();
+}
+
+mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream_t stream)
+{
+    if (!n || !n->Y || (!n->H && !n->Z && !n->A) || (n->A == nullptr) != (n->scaleA == nullptr) || n->top_k < 0 ||
+        (n->top_k > 0) != (n->pos != nullptr) || (n->top_k > 0) != (n->weights != nullptr) || !(n->eps > 0.0f))
+        return MXGEMM_ERR_INVALID_ARG;
+    const int bits = elem_bits(n->a_format);
+    if (!bits)
+        return MXGEMM_ERR_INVALID_ARG;
+    if (T < 1 || K < 32 || K % 32 || K > mx::kNormMaxK || n->ldy < K || (n->top_k > 0 && n->y_rows < 1) ||
+        (n->X && n->ldx < K) || (n->gate && n->ldg != 0 && n->ldg < K) || (n->H && n->ldh < K) || (n->Z && n->ldz < K))
+        return MXGEMM_ERR_SHAPE;
+    if (n->A) {
+        const mxgemm_status st = check_quantized(n->A, K, n->lda, n->ldsa, bits);
+        if (st != MXGEMM_OK)
+            return st;
+    }
+    const void *rows[] = {n->Y, n->X, n->gate, n->H, n->Z, n->w_post, n->w_pre};
+    const int64_t ld[] = {n->ldy, n->X ? n->ldx : 0, n->gate ? n->ldg : 0, n->H ? n->ldh : 0, n->Z ? n->ldz : 0, 0, 0};
+    for (int i = 0; i < 7; ++i)
+        if (!aligned(rows[i], 16) || ld[i] % 8)
+            return MXGEMM_ERR_ALIGN;
+    if (!aligned(n->pos, 4) || !aligned(n->weights, 4))
+        return MXGEMM_ERR_ALIGN;
+    const mxgemm_status st = mx::check_device();
+    if (st != MXGEMM_OK)
+        return st;
+    mx::NormArgs a;
+    a.Y = (const uint16_t *)n->Y;
+    a.pos = n->pos;
+    a.weights = n->weights;
+    a.w_post = (const uint16_t *)n->w_post;
+    a.gate = (const uint16_t *)n->gate;
+    a.X = (const uint16_t *)n->X;
+    a.w_pre = (const uint16_t *)n->w_pre;
+    a.H = (uint16_t *)n->H;
+    a.Z = (uint16_t *)n->Z;
+    a.A = (uint8_t *)n->A;
+    a.S = (uint8_t *)n->scaleA;
+    a.T = T;
+    a.K = K;
+    a.top_k = n->top_k;
+    a.y_rows = n->y_rows;
+    a.ldy = n->ldy;
+    a.ldg = n->ldg;
+    a.ldx = n->ldx;
+    a.ldh = n->ldh;
+    a.ldz = n->ldz;
+    a.lda_b = n->lda * bits / 8;
+    a.lds = n->ldsa;
+    a.res_scale = n->res_scale;
+    a.eps = n->eps;
+    a.fp8 = bits == 8;
+    mx::launch_norm(a, stream);
+    return launched();
+}
+
+mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const void *scaleA, const void *scaleB,
+                                 const int32_t *offsets, const int32_t *a_rows, float alpha, int rows, int a_count, int N,
+                                 int K, int groups, const mxgemm_grouped *strides, hipStream_t stream)
+{
+    if (!D || !A || !B || !scaleA || !scaleB || !offsets)
+        return MXGEMM_ERR_INVALID_ARG;
+    mxgemm_grouped s = {N, K, K / 32, K, K / 32, (int64_t)N * K, (int64_t)N * (K / 32), MXGEMM_FMT_FP4};
+    if (strides)
+        s = *strides;
+    const int bits = elem_bits(s.a_format);
+    if (!bits)
+        return MXGEMM_ERR_INVALID_ARG;
+    if (rows < 1 || a_count < 1 || (!a_rows && a_count < rows) || N < 1 || K < 32 || K % 32 || K > kMaxK || groups < 1 ||
+        groups > 65535 || s.ldd < N || s.lda < K || s.ldsa < K / 32 || s.ldb < K || s.ldsb < K / 32 || s.strideb < 0 ||
+        s.strideb_scale < 0)
+        return MXGEMM_ERR_SHAPE;
+    if (s.lda % 2 || s.ldb % 2 || s.strideb % 2 || !aligned(A, 16) || !aligned(B, 16) || (s.lda * bits) % 128 ||
+        (s.ldb / 2) % 16 || (s.strideb / 2) % 16 || !aligned(D, 2) || !aligned(offsets, 4) || !aligned(a_rows, 4))
+        return MXGEMM_ERR_ALIGN;
+    mx::GroupedArgs g;
+    g.lda_b = s.lda * bits / 8;
+    g.ldb_b = s.ldb / 2;
+    // the kernels address a tile's rows of B, and through a row list all of
+    // A, with 32-bit offsets
+    constexpr int64_t kSpan = (int64_t)1 << 31;
+    const int64_t a_span = a_rows ? a_count : 256;
+    if (g.lda_b >= kSpan / a_span || s.ldsa >= kSpan / a_span || g.ldb_b >= kSpan / 256 || s.ldsb >= kSpan / 256)
+        return MXGEMM_ERR_SHAPE;
+    int cu = 0;
+    const mxgemm_status st = mx::check_device(&cu);
+    if (st != MXGEMM_OK)
+        return st;
+    g.D = (uint16_t *)D;
+    g.A = (const uint8_t *)A;
+    g.B = (const uint8_t *)B;
+    g.SA = (const uint8_t *)scaleA;
+    g.SB = (const uint8_t *)scaleB;
+    g.offsets = offsets;
+    g.a_rows = a_rows;
+    g.alpha = alpha;
+    g.rows = rows;
+    g.a_count = a_count;
+    g.N = N;
+    g.K = K;
+    g.KB = K / 32;
+    g.E = groups;
+    g.ldd = s.ldd;
+    g.ldsa = s.ldsa;
+    g.ldsb = s.ldsb;
+    g.eb_b = s.strideb / 2;
+    g.esb = s.strideb_scale;
+    g.d_vec = aligned(D, 8) && s.ldd % 4 == 0;
+    g.d_stage = aligned(D, 16) && s.ldd % 8 == 0;
+    g.sa16 = g.KB % 16 == 0 && aligned(scaleA, 16) && s.ldsa % 16 == 0;
+    g.sb16 = g.KB % 16 == 0 && aligned(scaleB, 16) && s.ldsb % 16 == 0 && s.strideb_scale % 16 == 0;
+    g.fp8 = bits == 8;
+    mx::launch_grouped_stream(g, stream);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,173 @@
+"""Host-side checks of the mixture-of-experts entry points (no GPU): every
+refusal comes before any HIP call, struct layouts match the header, and the
+64-bit implementations the GPU tests compare with are checked themselves."""
+import ctypes
+import os
+import shutil
+import subprocess
+import tempfile
+
+import numpy as np
+import pytest
+
+import block_scaled_precision_mxfp4_amd as mx
+import experts_ref as ref
+import oracle
+from block_scaled_precision_mxfp4_amd import build as mxbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if mxbuild.is_stale():
+        mxbuild.build()
+
+
+def test_struct_layouts_match_the_header():
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    lines, want = [], []
+    for cname, cls in {"mxgemm_grouped": mx.Grouped, "mxgemm_norm": mx.Norm}.items():
+        lines.append('printf("%%zu\\n", sizeof(%s));' % cname)
+        want.append(ctypes.sizeof(cls))
+        for f, _ in cls._fields_:
+            lines.append('printf("%%zu\\n", offsetof(%s, %s));' % (cname, f))
+            want.append(getattr(cls, f).offset)
+    src = '#include <stdio.h>\n#include <stddef.h>\n#include "libmxgemm.h"\nint main(void){%s return 0;}\n' % " ".join(lines)
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(c, "w").write(src)
+        subprocess.run([cc, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + os.path.join(ROOT, "include"), c,
+                        "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == want
+
+
+REACHES_THE_DEVICE = (0, -4, -5)  # past every check: no device here (or it ran on a caller's GPU machine)
+
+
+def _route(**kw):
+    a = dict(ids=0x1000, weights=0x2000, pos=0x3000, offsets=0x4000, rows=0x5000, logits=0x6000, T=64, E=32, top_k=4,
+             workspace=None, workspace_bytes=0, stream=0)
+    a.update(kw)
+    return mx.mxgemm_route(**a, check=False)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(ids=None), -1), (dict(weights=None), -1), (dict(pos=None), -1), (dict(offsets=None), -1), (dict(rows=None), -1),
+    (dict(logits=None), -1), (dict(bf16=2), -1), (dict(renorm=-1), -1),
+    (dict(T=0), -2), (dict(E=0), -2), (dict(E=1025, ldl=1025), -2), (dict(top_k=0), -2), (dict(top_k=17), -2),
+    (dict(E=3), -2), (dict(ldl=31), -2), (dict(T=1 << 29, top_k=4), -2),
+    (dict(ids=0x1002), -3), (dict(weights=0x2001), -3), (dict(pos=0x3002), -3), (dict(offsets=0x4002), -3),
+    (dict(rows=0x5002), -3), (dict(logits=0x6002), -3), (dict(logits=0x6001, bf16=True), -3),
+    (dict(T=65), -6), (dict(T=65, workspace=0x7000, workspace_bytes=255), -6),
+    (dict(T=65, workspace=0x7002, workspace_bytes=256), -3),
+])
+def test_route_refusals(kw, code):
+    assert _route(**kw) == code
+
+
+def test_route_workspace_sizes():
+    assert mx.mxgemm_route_workspace_bytes(64, 1024) == 0
+    assert mx.mxgemm_route_workspace_bytes(0, 8) == 0 and mx.mxgemm_route_workspace_bytes(100, 1025) == 0
+    for T in (65, 128, 1000, 16384, 16385, 100000, 1 << 30):
+        for E in (1, 100, 1024):
+            n = mx.mxgemm_route_workspace_bytes(T, E)
+            assert 0 < n <= min(4 * E * -(-T // 64), 4 * E * 256)
+
+
+def _grouped(**kw):
+    a = dict(D=0x1000, A=0x2000, B=0x3000, scaleA=0x4000, scaleB=0x5000, offsets=0x6000, rows=64, N=256, K=512, groups=8,
+             stream=0)
+    a.update(kw)
+    return mx.mxgemm_grouped_run(**a, check=False)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(D=None), -1), (dict(A=None), -1), (dict(B=None), -1), (dict(scaleA=None), -1), (dict(scaleB=None), -1),
+    (dict(offsets=None), -1), (dict(a_format=2), -1), (dict(a_format=3), -1), (dict(a_format=-1), -1),
+    (dict(rows=0), -2), (dict(a_count=63), -2), (dict(a_rows=0x7000, a_count=0), -2), (dict(N=0), -2), (dict(K=48), -2),
+    (dict(K=16), -2), (dict(K=(1 << 24) + 32), -2), (dict(groups=0), -2), (dict(groups=65536), -2), (dict(ldd=255), -2),
+    (dict(lda=480), -2), (dict(ldsa=15), -2), (dict(ldb=480), -2), (dict(ldsb=15), -2), (dict(strideb=-32), -2),
+    (dict(strideb_scale=-1), -2), (dict(ldb=1 << 24), -2), (dict(ldsb=1 << 23), -2), (dict(lda=1 << 24), -2),
+    (dict(a_rows=0x7000, a_count=1 << 23), -2), (dict(a_rows=0x7000, a_count=1 << 10, ldsa=1 << 21), -2),
+    (dict(A=0x2008), -3), (dict(B=0x3008), -3), (dict(D=0x1001), -3), (dict(offsets=0x6002), -3), (dict(a_rows=0x7002), -3),
+    (dict(lda=513), -3), (dict(lda=528), -3), (dict(ldb=528), -3), (dict(strideb=256 * 512 + 16), -3),
+    (dict(a_format=1, lda=520), -3),
+])
+def test_grouped_refusals(kw, code):
+    assert _grouped(**kw) == code
+
+
+def _glu(**kw):
+    a = dict(A=0x1000, scaleA=0x2000, X=0x3000, M=4, K=64, stream=0)
+    a.update(kw)
+    return mx.mxgemm_glu_quantize(**a, check=False)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(A=None), -1), (dict(scaleA=None), -1), (dict(X=None), -1), (dict(a_format=2), -1), (dict(a_format=4), -1),
+    (dict(M=0), -2), (dict(K=0), -2), (dict(K=48), -2), (dict(K=(1 << 24) + 32), -2), (dict(ldx=120), -2), (dict(lda=32), -2),
+    (dict(ldsa=1), -2), (dict(M=1 << 30, K=1 << 20), -2),
+    (dict(X=0x3008), -3), (dict(ldx=132), -3), (dict(A=0x1008), -3), (dict(lda=80), -3), (dict(a_format=1, lda=72), -3),
+    (dict(live=0x4002), -3),
+])
+def test_glu_refusals(kw, code):
+    assert _glu(**kw) == code
+
+
+def _norm(**kw):
+    a = dict(T=4, K=64, Y=0x1000, X=0x2000, H=0x3000, Z=0x4000, A=0x5000, scaleA=0x6000, w_post=0x7000, w_pre=0x8000,
+             stream=0)
+    a.update(kw)
+    return mx.mxgemm_norm_quantize(**a, check=False)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Y=None), -1), (dict(H=None, Z=None, A=None, scaleA=None), -1), (dict(A=None), -1), (dict(scaleA=None), -1),
+    (dict(top_k=-1), -1), (dict(top_k=2), -1), (dict(top_k=2, pos=0x9000), -1), (dict(pos=0x9000, weights=0xA000), -1),
+    (dict(eps=0.0), -1), (dict(eps=float("nan")), -1), (dict(a_format=2), -1),
+    (dict(T=0), -2), (dict(K=0), -2), (dict(K=48), -2), (dict(K=16416), -2), (dict(ldy=32), -2), (dict(ldx=32), -2),
+    (dict(gate=0x9000, ldg=32), -2), (dict(ldh=32), -2), (dict(ldz=32), -2), (dict(lda=32), -2), (dict(ldsa=1), -2),
+    (dict(top_k=2, pos=0x9000, weights=0xA000, y_rows=0), -2),
+    (dict(Y=0x1008), -3), (dict(X=0x2008), -3), (dict(gate=0x9008), -3), (dict(H=0x3002), -3), (dict(Z=0x4008), -3),
+    (dict(A=0x5008), -3), (dict(w_post=0x7008), -3), (dict(w_pre=0x8008), -3), (dict(ldy=68), -3), (dict(ldx=68), -3),
+    (dict(gate=0x9000, ldg=68), -3), (dict(ldh=68), -3), (dict(ldz=68), -3), (dict(lda=80), -3),
+    (dict(top_k=2, pos=0x9002, weights=0xA000, y_rows=9), -3), (dict(top_k=2, pos=0x9000, weights=0xA001, y_rows=9), -3),
+])
+def test_norm_refusals(kw, code):
+    assert _norm(**kw) == code
+
+
+# ---- the 64-bit implementations themselves ------------------------------------
+
+def test_bf16_rounding_matches_torch():
+    torch = pytest.importorskip("torch")
+    rng = np.random.default_rng(1)
+    f = np.concatenate([rng.integers(0, 1 << 32, 200000, dtype=np.uint32).view(np.float32),
+                        np.array([1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8, 3.3961775e38, 3.39e38, 2.0 ** -133, 1.5 * 2.0 ** -133], np.float32)])
+    f = f[~np.isnan(f)]
+    want = torch.from_numpy(f).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+    assert np.array_equal(ref.f64_to_bf16(f.astype(np.float64)), want)
+
+
+def test_fp8_quantizer_matches_torch_casts():
+    torch = pytest.importorskip("torch")
+    rng = np.random.default_rng(2)
+    bits = ref.f64_to_bf16(rng.standard_normal((64, 256)) * np.exp2(rng.uniform(-140, 120, (64, 1))))
+    code, scale = ref.quantize_fp8(bits)
+    v = ref.bf16_to_f64(bits).reshape(64, -1, 32)
+    x = scale.astype(int) - 127
+    most = np.abs(v).max(-1)
+    assert ((most == 0) | (x == -127) | ((np.ldexp(most, -x) >= 256) & (np.ldexp(most, -x) < 512))).all()
+    s = torch.from_numpy(np.clip(np.ldexp(v, -x[..., None]), -448, 448).reshape(64, 256).astype(np.float32))
+    assert np.array_equal(code, s.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_fp8_codes_decode_to_their_values():
+    bits = ref.f64_to_bf16(np.linspace(-300, 300, 64).reshape(1, 64))
+    code, scale = ref.quantize_fp8(bits)
+    got = np.array([oracle.decode(1, int(c)) for c in code[0]]) * np.exp2(scale[0].astype(float) - 127).repeat(32)
+    assert np.abs(got - ref.bf16_to_f64(bits)[0]).max() <= 2.0 ** -4 * 300
