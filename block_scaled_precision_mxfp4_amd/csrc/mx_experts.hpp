@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "mx_args.hpp"
+
 namespace mx {
 
 // ---- router choice (mx_route.hip)
@@ -59,19 +61,26 @@ struct NormArgs {
 };
 void launch_norm(const NormArgs &n, hipStream_t s);
 
-// ---- product grouped by expert (mx_grouped.hip)
-struct GroupedArgs {
-    uint16_t *D;             // bf16 [rows][ldd]
-    const uint8_t *A, *B, *SA, *SB;
+// ---- product grouped by expert
+// The tiled kernel's arguments (mx_tile.hip: GemmArgs with M = rows of D, no
+// C, unsplit, row-major operands) and what the groups add.
+struct GroupedTileArgs : GemmArgs {
     const int32_t *offsets;  // [E + 1]
-    const int32_t *a_rows;   // [rows] or null
-    float alpha;
-    int rows, a_count, N, K, KB, E;
-    int64_t ldd, lda_b, ldsa, ldb_b, ldsb, eb_b, esb;  // bytes (ldd: elements); eb_b, esb: expert to expert
-    int d_vec, d_stage;      // 8-byte D stores; 16-byte D rows
-    int sa16, sb16;          // scale rows in 16-byte aligned groups of 16 K-blocks
-    int fp8;
+    const int32_t *a_rows;   // [M] or null
+    int a_count, E;
+    int64_t eb_b, esb;       // bytes from one expert's B, and scales, to the next's
 };
-void launch_grouped_stream(const GroupedArgs &g, hipStream_t s);
+// Experts that the persistent tiled kernel keeps a table of in LDS.
+constexpr int kGroupTable = 1024;
+typedef void (*GroupedLaunchFn)(const GroupedTileArgs &, int64_t grid, hipStream_t);
+struct GroupedTileKernel {
+    int bm, bn;
+    GroupedLaunchFn launch[2];   // FP4 A, FP8 E4M3 A (may be null)
+    GroupedLaunchFn persist[2];  // persistent (may be null): aligned scale rows, K % 512 == 0, 16-byte rows of D,
+                                 // N % 8 == 0, at most kGroupTable experts
+};
+const GroupedTileKernel *grouped_tile_kernels(int *count);
+// Few rows per expert (mx_grouped.hip)
+void launch_grouped_stream(bool fp8, const GroupedTileArgs &g, hipStream_t s);
 
 }  // namespace mx

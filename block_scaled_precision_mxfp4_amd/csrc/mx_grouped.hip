@@ -10,38 +10,14 @@
 // An expert with more than 16 MG rows is done in several passes over B.
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
+#include "mx_group.hpp"
 
 #include <type_traits>
 
 namespace mx {
 
-// The nth expert that has rows (from 0): its number and row range; false if
-// there are fewer.  By one wave, the same result in every lane.  Offsets are
-// clamped to [0, rows].
-__device__ __forceinline__ bool nth_group(const int32_t *offsets, int E, int rows, int nth, int lane, int &e, int &m0,
-                                          int &m1)
-{
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int i = e0 + lane;
-        const int lo = i < E ? min(max(offsets[i], 0), rows) : 0;
-        const int hi = i < E ? min(max(offsets[i + 1], 0), rows) : 0;
-        const uint64_t some = __ballot(hi > lo);
-        const int n = __popcll(some);
-        if (nth < n) {
-            const bool it = hi > lo && __popcll(some & ((1ull << lane) - 1)) == nth;
-            const int at = __ffsll((unsigned long long)__ballot(it)) - 1;
-            e = e0 + at;
-            m0 = __builtin_amdgcn_readlane(lo, at);
-            m1 = __builtin_amdgcn_readlane(hi, at);
-            return true;
-        }
-        nth -= n;
-    }
-    return false;
-}
-
 template <bool FP8, int MG, int NR, bool SVEC>
-__global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
+__global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedTileArgs g)
 {
     using a_t = typename std::conditional<FP8, v8i, v4i>::type;
     constexpr int AKB = FP8 ? 32 : 16;  // bytes of an A K-block
@@ -49,7 +25,7 @@ __global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int e, m0, m1;
-    if (!nth_group(g.offsets, g.E, g.rows, blockIdx.y, lane, e, m0, m1))
+    if (!nth_group(g.offsets, g.E, g.M, blockIdx.y, lane, e, m0, m1))
         return;
     const int n0 = blockIdx.x * 16 * NR;
     const int rows_b = min(16 * NR, g.N - n0);
@@ -155,18 +131,18 @@ __global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
 }
 
 template <bool FP8, int MG, int NR>
-static void launch_stream_as(const GroupedArgs &g, hipStream_t s)
+static void launch_stream_as(const GroupedTileArgs &g, hipStream_t s)
 {
-    const dim3 grid((unsigned)((g.N + 16 * NR - 1) / (16 * NR)), (unsigned)(g.E < g.rows ? g.E : g.rows));
-    if (g.sa16 && g.sb16)
+    const dim3 grid((unsigned)((g.N + 16 * NR - 1) / (16 * NR)), (unsigned)(g.E < g.M ? g.E : g.M));
+    if (g.scale16)
         hipLaunchKernelGGL((mx_grouped_stream_kernel<FP8, MG, NR, true>), grid, dim3(256), 0, s, g);
     else
         hipLaunchKernelGGL((mx_grouped_stream_kernel<FP8, MG, NR, false>), grid, dim3(256), 0, s, g);
 }
 
-void launch_grouped_stream(const GroupedArgs &g, hipStream_t s)
+void launch_grouped_stream(bool fp8, const GroupedTileArgs &g, hipStream_t s)
 {
-    if (g.fp8)
+    if (fp8)
         launch_stream_as<true, 1, 1>(g, s);
     else
         launch_stream_as<false, 1, 1>(g, s);

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "mx_args.hpp"
 #include "mx_experts.hpp"
@@ -42,6 +43,27 @@ int route_blocks(int T)
 {
     const int per = route_units_per_block(T);
     return (route_units(T) + per - 1) / per;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The grouped product's kernel: an index into the tiles, or -1 for streaming.
+int plan_grouped(int rows, int N, int K, int groups, int bits, const mx::GroupedTileKernel *tiles, int n_tiles)
+{
+    if (K < 256)  // (the tiled kernel reads scale rows 8 bytes at a time)
+        return -1;
+    if (const char *e = std::getenv("MXGEMM_GROUPED_TILE")) {
+        const int k = std::atoi(e);
+        if (k < n_tiles && (k < 0 || tiles[k].launch[bits == 8]))
+            return k;
+    }
+    const double per = (double)rows / groups;
+    if (per <= 16)
+        return -1;
+    for (int k = 0; k < n_tiles; ++k)
+        if (tiles[k].launch[bits == 8] && per >= tiles[k].bm)
+            return k;
+    return n_tiles - 1;
 }
 
 }  // namespace
@@ -209,7 +231,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     if (s.lda % 2 || s.ldb % 2 || s.strideb % 2 || !aligned(A, 16) || !aligned(B, 16) || (s.lda * bits) % 128 ||
         (s.ldb / 2) % 16 || (s.strideb / 2) % 16 || !aligned(D, 2) || !aligned(offsets, 4) || !aligned(a_rows, 4))
         return MXGEMM_ERR_ALIGN;
-    mx::GroupedArgs g;
+    mx::GroupedTileArgs g = {};
     g.lda_b = s.lda * bits / 8;
     g.ldb_b = s.ldb / 2;
     // the kernels address a tile's rows of B, and through a row list all of
@@ -218,10 +240,6 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     const int64_t a_span = a_rows ? a_count : 256;
     if (g.lda_b >= kSpan / a_span || s.ldsa >= kSpan / a_span || g.ldb_b >= kSpan / 256 || s.ldsb >= kSpan / 256)
         return MXGEMM_ERR_SHAPE;
-    int cu = 0;
-    const mxgemm_status st = mx::check_device(&cu);
-    if (st != MXGEMM_OK)
-        return st;
     g.D = (uint16_t *)D;
     g.A = (const uint8_t *)A;
     g.B = (const uint8_t *)B;
@@ -230,7 +248,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     g.offsets = offsets;
     g.a_rows = a_rows;
     g.alpha = alpha;
-    g.rows = rows;
+    g.M = rows;
     g.a_count = a_count;
     g.N = N;
     g.K = K;
@@ -241,12 +259,41 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     g.ldsb = s.ldsb;
     g.eb_b = s.strideb / 2;
     g.esb = s.strideb_scale;
+    g.split = 1;
     g.d_vec = aligned(D, 8) && s.ldd % 4 == 0;
     g.d_stage = aligned(D, 16) && s.ldd % 8 == 0;
-    g.sa16 = g.KB % 16 == 0 && aligned(scaleA, 16) && s.ldsa % 16 == 0;
-    g.sb16 = g.KB % 16 == 0 && aligned(scaleB, 16) && s.ldsb % 16 == 0 && s.strideb_scale % 16 == 0;
-    g.fp8 = bits == 8;
-    mx::launch_grouped_stream(g, stream);
+    auto scale_rows = [&](const void *p, int64_t ld, int64_t n) { return g.KB % n == 0 && aligned(p, n) && ld % n == 0; };
+    g.scale16 = scale_rows(scaleA, s.ldsa, 16) && scale_rows(scaleB, s.ldsb, 16) && s.strideb_scale % 16 == 0;
+    g.group_m = 8;
+
+    int n_tiles = 0;
+    const mx::GroupedTileKernel *tiles = mx::grouped_tile_kernels(&n_tiles);
+    const int kernel = plan_grouped(rows, N, K, groups, bits, tiles, n_tiles);
+    if (kernel >= 0) {
+        const mx::GroupedTileKernel &t = tiles[kernel];
+        const int64_t some = std::min(rows, groups);  // experts that can have rows
+        const int64_t grid = ((rows - some) / t.bm + some) * cdiv(N, t.bn);
+        if (grid > kMaxGrid)
+            return MXGEMM_ERR_SHAPE;
+        g.tiles_n = cdiv(N, t.bn);
+        int cu = 0;
+        const mxgemm_status st = mx::check_device(&cu);
+        if (st != MXGEMM_OK)
+            return st;
+        const char *e = std::getenv("MXGEMM_TILE_PERSIST");
+        if (t.persist[bits == 8] && !(e && *e == '0') && grid > cu && g.scale16 && g.d_stage &&
+            N % 8 == 0 && groups <= mx::kGroupTable && s.ldd < ((int64_t)1 << 21))
+            t.persist[bits == 8](g, cu, stream);
+        else
+            t.launch[bits == 8](g, grid, stream);
+    } else {
+        if (cdiv(N, 16) > kMaxGrid)
+            return MXGEMM_ERR_SHAPE;
+        const mxgemm_status st = mx::check_device();
+        if (st != MXGEMM_OK)
+            return st;
+        mx::launch_grouped_stream(bits == 8, g, stream);
+    }
     return launched();
 }
 
