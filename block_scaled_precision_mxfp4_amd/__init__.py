@@ -164,8 +164,10 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
+        # torch.cuda.current_stream().cuda_stream without building the Stream
+        # object (0.3 against 2.8 us, as much as the launch itself)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

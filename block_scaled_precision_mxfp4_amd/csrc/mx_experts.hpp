@@ -75,6 +75,7 @@ constexpr int kGroupTable = 1024;
 typedef void (*GroupedLaunchFn)(const GroupedTileArgs &, int64_t grid, hipStream_t);
 struct GroupedTileKernel {
     int bm, bn;
+    int min_rows[2];             // rows per expert from which it is taken: FP4 A, FP8 E4M3 A
     GroupedLaunchFn launch[2];   // FP4 A, FP8 E4M3 A (may be null)
     GroupedLaunchFn persist[2];  // persistent (may be null): aligned scale rows, K % 512 == 0, 16-byte rows of D,
                                  // N % 8 == 0, at most kGroupTable experts

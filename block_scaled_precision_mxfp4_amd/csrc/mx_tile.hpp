@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     constexpr int TM = BM / WM, TN = BN / WN;  // wave tile
     constexpr int FM = TM / 16, FN = TN / 16;  // 16-row fragments per wave
     static_assert(NW == 4 || NW == 8, "four or eight waves");
-    static_assert(FM % 2 == 0 && FN % 2 == 0, "scale words cover 32-row groups");
+    static_assert(GROUPED || (FM % 2 == 0 && FN % 2 == 0), "scale words cover 32-row groups");
     constexpr uint32_t kFar = 0x80000100u;  // past every range, also with a stage's offsets added
     // bytes per stage (dense FP6 A: 16-row groups of two 1536-byte steps)
     constexpr int A_STAGE = A6D ? BM * 192 : BM * 128 * AREG, B_STAGE = BN * 128;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     uint32_t sbp[SBP_PER_THREAD], sap[SAP_PER_THREAD];
     // dense FP6: this wave's packed scale words of a stage (its 32-row groups
     // of A and of B), one register set per buffer
-    uint32_t rsaw[2][FM / 2], rsbw[2][FN / 2];
+    uint32_t rsaw[2][(FM + 1) / 2], rsbw[2][(FN + 1) / 2];
     auto issue_scales = [&](int kt, bool on, auto bufc) __attribute__((always_inline)) {
         constexpr int BUF = decltype(bufc)::value;
         const int kb_s = kb_begin + kt * 8;
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
         const uint8_t *sa_tile = BUF ? s_a1 : s_a0;
         const uint8_t *sb_tile = BUF ? s_b1 : s_b0;
         const uint32_t *ssc = BUF ? s_sc1 : s_sc0;
-        uint32_t saw[FM / 2], sbw[FN / 2];
+        uint32_t saw[(FM + 1) / 2], sbw[(FN + 1) / 2];
         if constexpr (!GROUPED) {
 #pragma unroll
         for (int p = 0; p < FM / 2; ++p)
