@@ -3,11 +3,9 @@
 // MXFP8, in one pass: v itself never reaches memory.
 //
 // silu(g) u = g u / (1 + e^-g).  v is the correctly rounded bf16 value, so
-// that codes and scales do not depend on how the exponential was computed:
-// the fp32 evaluation is within 6 units in its last place, and only where
-// that leaves the bf16 rounding open (its low 16 bits within 8 of a half, 1
-// element in 4000), or where its range does not carry it, the element is
-// evaluated again in 64 bits.
+// that codes and scales do not depend on how the exponential was computed: it
+// is evaluated in fp32, and again in 64 bits only where fp32's error leaves
+// the bf16 rounding open (1 element in 4000) or its range does not carry it.
 //
 // Bound by HBM: 4 bytes read and 17/32 (FP4) or 33/32 (FP8) byte written per
 // element, each once.  Four lanes share a block and hold 8 elements each.
@@ -17,84 +15,93 @@
 
 namespace mx {
 
-__device__ __noinline__ float glu_f64(float g, float u)
+// The value in 64 bits.  Zeros of finite factors are what they are.
+__device__ __noinline__ float glu_f64(float g, float u, float v)
 {
+    if (v == 0.0f && (g == 0.0f || u == 0.0f))
+        return v;
     return f32_for_bf16((double)g / (1.0 + exp(-(double)g)) * (double)u);
 }
 
-__device__ __forceinline__ float glu_f32(float g, float u)
+// 8 values of a lane.  fp32's error: the argument of the exponential is kept
+// to twice fp32's bits (hi + lo = -g log2 e), exp2 and rcp are within one unit
+// in the last place, the five roundings around them half a unit each, so v is
+// within 6 units.  `open`: the low 16 bits are within 8 units of a half, or |g|
+// is above 64 (the exponential may overflow), or |g| or |v| below 2^-98 (fp32
+// may lose bits on the way; for |g| <= 64 silu(g) is no smaller than |g| / 2 or
+// 2^-87).  Infinite or NaN products are the same in both.  The 8 tests are
+// made as one first: 1 group of 8 in 500 fails it.
+__device__ __forceinline__ v4i glu_8(v4i xg, v4i xu)
 {
-    // e^-g = 2^hi * (1 + lo ln 2): hi + lo = -g log2 e to twice fp32's bits
     const float c = -1.44269504088896341f, c_lo = -1.92596299112661746887e-8f;
-    const float hi = g * c;
-    const float lo = fmaf(g, c_lo, fmaf(g, c, -hi));
-    float e = __builtin_amdgcn_exp2f(hi);
-    e = fmaf(e, lo * 0.69314718055994531f, e);
-    const float s = g * __builtin_amdgcn_rcpf(1.0f + e);
-    const float v = s * u;
-    const uint32_t low = __float_as_uint(v) & 0xFFFFu;
-    // beyond |g| = 64 or below 2^-100 (also infinities and NaN) fp32 may lose
-    // the value on the way
-    const bool tiny = !(fabsf(s) >= 0x1p-100f) || !(fabsf(v) >= 0x1p-120f);
-    const bool zero = v == 0.0f && (g == 0.0f || u == 0.0f);
-    const bool open = low - 0x7FF8u <= 16u || !(fabsf(g) <= 64.0f) || (tiny && !zero);
-    return open ? glu_f64(g, u) : v;
+    constexpr uint32_t kNear = 16u << 16;
+    float g[8], u[8], v[8];
+    uint32_t near = 0xFFFFFFFFu;
+    float most = 0.0f, least = 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t g2 = (uint32_t)xg[i >> 1], u2 = (uint32_t)xu[i >> 1];
+        g[i] = __uint_as_float(i & 1 ? g2 & 0xFFFF0000u : g2 << 16);
+        u[i] = __uint_as_float(i & 1 ? u2 & 0xFFFF0000u : u2 << 16);
+        const float hi = g[i] * c;
+        const float lo = fmaf(g[i], c_lo, fmaf(g[i], c, -hi));
+        float e = __builtin_amdgcn_exp2f(hi);
+        e = fmaf(e, lo * 0.69314718055994531f, e);
+        v[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
+        near = min(near, (__float_as_uint(v[i]) - 0x7FF8u) << 16);
+        most = fmaxf(most, fabsf(g[i]));
+        least = fminf(least, fminf(fabsf(g[i]), fabsf(v[i])));
+    }
+    if (near <= kNear || most > 64.0f || least < 0x1p-98f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool open = (__float_as_uint(v[i]) - 0x7FF8u) << 16 <= kNear || !(fabsf(g[i]) <= 64.0f) ||
+                              !(fminf(fabsf(g[i]), fabsf(v[i])) >= 0x1p-98f);
+            if (open)
+                v[i] = glu_f64(g[i], u[i], v[i]);
+        }
+    }
+    v4i out;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        out[w] = (int)bf16x2_rne(v[2 * w], v[2 * w + 1]);
+    return out;
 }
 
-template <int U, bool FP8>
+// A workgroup takes 64 blocks, one for each four lanes.  One block a lane
+// group and a workgroup per 64, against 2 and 4 blocks: 32768 x 2048 67.3 us
+// against 69.3 and 71.2 (FP4; 4.2 TB/s), 65.1 against 71.5 and 74.0 (FP8), 256 x
+// 2048 4.4 against 6.1 and 9.6.
+template <bool FP8>
 __global__ void __launch_bounds__(256) mx_glu_kernel(GluArgs q)
 {
-    const int j = threadIdx.x & 3, grp = threadIdx.x >> 2;
+    const int j = threadIdx.x & 3;
+    const int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
     const int kbn = q.K >> 5;
-    const int64_t b0 = (int64_t)blockIdx.x * (64 * U) + grp;
     const int64_t live_rows = q.live ? min((int64_t)max(*q.live, 0), (int64_t)q.M) : q.M;
-    int64_t row = b0 / kbn;
-    int col = (int)(b0 - row * kbn);
-    const int drow = 64 / kbn, dcol = 64 % kbn;
-    v4i xg[U], xu[U];
-    int64_t r[U];
-    int kb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool on = row < live_rows;
-        r[u] = on ? row : -1;
-        kb[u] = col;
-        const uint16_t *p = q.X + row * q.ldx + col * 32 + j * 8;
-        xg[u] = on ? __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p)) : v4i{0, 0, 0, 0};
-        xu[u] = on ? __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p + q.K)) : v4i{0, 0, 0, 0};
-        row += drow;
-        col += dcol;
-        if (col >= kbn) {
-            col -= kbn;
-            ++row;
-        }
+    // (64-bit division is a long sequence: only where the count needs it)
+    const int64_t row = q.blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)b / (uint32_t)kbn) : b / kbn;
+    const int elem = (int)(b - row * kbn) * 32 + j * 8;
+    const bool on = row < live_rows;
+    v4i xg = {0, 0, 0, 0}, xu = xg;
+    if (on) {
+        const uint16_t *p = q.X + row * q.ldx + elem;
+        xg = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p));
+        xu = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p + q.K));
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        v4i v;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t g2 = (uint32_t)xg[u][w], u2 = (uint32_t)xu[u][w];
-            const float lo = glu_f32(bf16_to_f32(g2 & 0xFFFFu), bf16_to_f32(u2 & 0xFFFFu));
-            const float hi = glu_f32(bf16_to_f32(g2 >> 16), bf16_to_f32(u2 >> 16));
-            v[w] = (int)bf16x2_rne(lo, hi);
-        }
-        // (a dead row's addresses are not used)
-        const int64_t rr = r[u] < 0 ? 0 : r[u];
-        quantize_store<FP8>(v, q.A + rr * q.lda_b, q.S + rr * q.lds, kb[u] * 32 + j * 8, r[u] >= 0);
-    }
+    const int64_t r = on ? row : 0;  // (a dead row's addresses are not used)
+    quantize_store<FP8>(glu_8(xg, xu), q.A + r * q.lda_b, q.S + r * q.lds, elem, on);
 }
 
-constexpr int kGluU = 2;
-int64_t glu_grid(int64_t blocks) { return (blocks + 64 * kGluU - 1) / (64 * kGluU); }
+int64_t glu_grid(int64_t blocks) { return (blocks + 63) / 64; }
 
 void launch_glu(const GluArgs &g, hipStream_t s)
 {
     const dim3 grid((unsigned)glu_grid(g.blocks));
     if (g.fp8)
-        hipLaunchKernelGGL((mx_glu_kernel<kGluU, true>), grid, dim3(256), 0, s, g);
+        hipLaunchKernelGGL(mx_glu_kernel<true>, grid, dim3(256), 0, s, g);
     else
-        hipLaunchKernelGGL((mx_glu_kernel<kGluU, false>), grid, dim3(256), 0, s, g);
+        hipLaunchKernelGGL(mx_glu_kernel<false>, grid, dim3(256), 0, s, g);
 }
 
 }  // namespace mx

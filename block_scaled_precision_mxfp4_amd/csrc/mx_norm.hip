@@ -27,14 +27,37 @@ __device__ __forceinline__ double bf16_at(v4i x, int i)
     return (double)bf16_to_f32(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
 }
 
+__device__ __forceinline__ double dpp_f64(double v, int step)
+{
+    const uint64_t u = __double_as_longlong(v);
+    const uint32_t lo = row_partner((uint32_t)u, step), hi = row_partner((uint32_t)(u >> 32), step);
+    return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+
+// Sum over a wave, the same bits in every lane: four steps inside 16 lanes by
+// row permutes, then the four rows' sums in order.
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v += dpp_f64(v, i);
+    const uint64_t u = __double_as_longlong(v);
+    double t = 0.0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, 16 * r);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), 16 * r);
+        t += __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+    }
+    return t;
+}
+
 // Sum over the workgroup, the same bits in every thread; s: NW doubles of its
 // own (two sums in a row use different ones).
 template <int NW>
 __device__ __forceinline__ double block_sum(double v, double *s)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2)
-        v += __shfl_xor(v, d);
+    v = wave_sum(v);
     if constexpr (NW == 1)
         return v;
     if ((threadIdx.x & 63) == 0)
@@ -76,18 +99,34 @@ __global__ void __launch_bounds__(NT) mx_norm_kernel(NormArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 y[c][i] = 0.0;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int p = a.pos[t * a.top_k + j];
-            if (p < 0 || p >= a.y_rows)  // not routed (or no row of Y)
-                continue;
-            const double w = (double)a.weights[t * a.top_k + j];
+        // U rows at a time, all of their loads in flight together.  A row
+        // that is not there reads as zeros (row 0 is read in its place: what
+        // it holds does not matter, also a NaN).
+        constexpr int U = C == 1 ? 4 : 2;
+        for (int j0 = 0; j0 < a.top_k; j0 += U) {
+            v4i r[U][C];
+            double w[U];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const v4i r = load(a.Y + (int64_t)p * a.ldy, c);
+            for (int i = 0; i < U; ++i) {
+                const int64_t at = t * a.top_k + min(j0 + i, a.top_k - 1);
+                const int p = a.pos[at];
+                const bool ok = j0 + i < a.top_k && (uint32_t)p < (uint32_t)a.y_rows;
+                w[i] = (double)a.weights[at];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[c][i] = fma(w, bf16_at(r, i), y[c][i]);
+                for (int c = 0; c < C; ++c) {
+                    r[i][c] = load(a.Y + (int64_t)(ok ? p : 0) * a.ldy, c);
+                    if (!ok)
+                        r[i][c] = zero;
+                }
+                w[i] = ok ? w[i] : 0.0;
             }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int x8 = 0; x8 < 8; ++x8)
+                        y[c][x8] = fma(w[i], bf16_at(r[i][c], x8), y[c][x8]);
         }
     } else {
 #pragma unroll

@@ -25,23 +25,11 @@
 
 namespace mx {
 
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v, int step)
-{
-    // partner of step 0..3 inside 16 lanes: lane ^ 1, lane ^ 2, the mirrored
-    // lane of 8 and of 16 (whose quads and halves already agree)
-    switch (step) {
-    case 0: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
-    case 1: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
-    case 2: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);
-    default: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);
-    }
-}
-
 __device__ __forceinline__ uint32_t row_max(uint32_t v)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        v = max(v, dpp_u32(v, i));
+        v = max(v, row_partner(v, i));
     return v;
 }
 
@@ -49,7 +37,7 @@ __device__ __forceinline__ uint32_t row_min(uint32_t v)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        v = min(v, dpp_u32(v, i));
+        v = min(v, row_partner(v, i));
     return v;
 }
 
@@ -57,7 +45,7 @@ __device__ __forceinline__ float row_sum(float v)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        v += __uint_as_float(dpp_u32(__float_as_uint(v), i));
+        v += __uint_as_float(row_partner(__float_as_uint(v), i));
     return v;
 }
 
@@ -279,10 +267,19 @@ __global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
     const int e = tid & (ep - 1);
     if (e < E) {
         int total = 0, before = 0;
-        for (int b = tid / ep; b < r.blocks; b += 1024 / ep) {
-            const int c = r.counts[(int64_t)b * E + e];
-            total += c;
-            before += b < (int)blockIdx.x ? c : 0;
+        // (a batch's loads are in flight together)
+        for (int b0 = tid / ep; b0 < r.blocks; b0 += 8 * (1024 / ep)) {
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int b = b0 + i * (1024 / ep);
+                c[i] = b < r.blocks ? r.counts[(int64_t)b * E + e] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                total += c[i];
+                before += b0 + i * (1024 / ep) < (int)blockIdx.x ? c[i] : 0;
+            }
         }
         atomicAdd(&s_total[e], total);
         atomicAdd(&s_before[e], before);
