@@ -72,15 +72,24 @@ __device__ __forceinline__ ScaleRows load_scale_rows(__amdgpu_buffer_rsrc_t r, i
     return s;
 }
 
-// A row's 8 stage scale bytes at any alignment, blocks at or past KB (>= 8) as
-// zero: one load that ends at the row's end at the latest, shifted.
-__device__ __forceinline__ v2u load_scale_row_any(const uint8_t *row, int kb_s, int KB)
+// (of known address space: a load through a pointer made from an integer
+// would also take the LDS's path)
+typedef __attribute__((address_space(1))) uint8_t global_u8;
+
+// A row's scale bytes of 8 K-blocks from kb on at any alignment: one load that
+// ends at the row's end (KB >= 8 blocks) at the latest, to be shifted by
+// scale_row_shift.  base is wave-uniform, row the lane's offset.
+__device__ __forceinline__ uint64_t load_scale_row_any(const global_u8 *base, uint32_t row, int kb, int KB)
 {
-    const int at = min(kb_s, KB - 8);
-    uint64_t w;
-    __builtin_memcpy(&w, row + at, 8);
-    w = kb_s - at < 8 ? w >> (8 * (kb_s - at)) : 0;
-    return v2u{(uint32_t)w, (uint32_t)(w >> 32)};
+    typedef uint64_t __attribute__((aligned(1))) any_u64;
+    return *reinterpret_cast<const __attribute__((address_space(1))) any_u64 *>(base + min(kb, KB - 8) + row);
+}
+
+// ... to block kb's byte first and zeros for blocks at or past KB.
+__device__ __forceinline__ uint64_t scale_row_shift(uint64_t w, int kb, int KB)
+{
+    const int past = kb - min(kb, KB - 8);
+    return past < 8 ? w >> (8 * past) : 0;
 }
 
 // Word for lane (K-block d5 of the step, row d2): bytes
@@ -201,7 +210,11 @@ __device__ __forceinline__ void store_range_tile_staged(__amdgpu_buffer_rsrc_t r
 // GROUPED: the product grouped by expert (row-major operands, unsplit): the
 // tile's expert and rows come from the offsets, its rows of A through the row
 // list where there is one (a lane's row offsets, kept in registers, take the
-// place of the row pitch).  The row list, the offsets and the experts'
+// place of the row pitch).  Without aligned scale rows (SVEC) the codes past
+// K, those of the next row or of its padding, are multiplied, by the scale
+// bytes 0 that stand there for both operands: 2^-254 times at most 36 * 32 is
+// below half of fp32's least value, so that nothing is added.  An 8-bit A may
+// hold a NaN there and is masked.  The row list, the offsets and the experts'
 // strides are in GroupedTileArgs.  Its persistent form takes partial tiles:
 // D goes out with range-checked buffer stores, so that every wave issues
 // STORES of them whatever part of the tile is inside; the experts' table is
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     // XB); the expert's end
     uint32_t a_row[GROUPED ? A_CH / NW : 1], x_row = 0;
     int m_end = 0;
-    const uint8_t *x_base = nullptr;
+    const global_u8 *x_base = nullptr;
     constexpr bool TABLE = GROUPED && PERSIST;
     __shared__ int s_lo[TABLE ? kGroupTable : 1], s_hi[TABLE ? kGroupTable : 1], s_upto[TABLE ? kGroupTable : 1];
     __shared__ int s_total;
@@ -349,7 +362,11 @@ __global__ void __launch_bounds__(64 * WM * WN)
     auto load_group_src = [&](auto &ga) __attribute__((always_inline)) {
         kb_begin = 0;
         kb_end = ga.KB;
+        // (the persistent form needs an even count: a stage past K multiplies
+        // zeros)
         nst = (kb_end + 7) >> 3;
+        if constexpr (PERSIST)
+            nst += nst & 1;
         // without a row list the tile's own rows, from its first one on
         const int64_t first = ga.a_rows ? 0 : m0;
         const int rows_a = ga.a_rows ? ga.a_count : min(BM, m_end - m0);
@@ -371,8 +388,11 @@ __global__ void __launch_bounds__(64 * WM * WN)
         const int64_t ldx = xa ? ga.ldsa : ga.ldsb;
         const bool x_in = (xa ? u < BM : xb && u < BN) && (uint32_t)raw_x < (uint32_t)rows_x;
         x_row = x_in ? (uint32_t)(raw_x * ldx) : SVEC ? kFar : 0u;
-        x_base = xa ? ga.SA + first * ga.ldsa : ga.SB + e * ga.esb + n0 * ga.ldsb;
-        rsa = make_rsrc_u(x_base, xa || xb ? (uint32_t)((rows_x - 1) * ldx + ga.KB) : 0u);
+        const uint64_t xp = (uint64_t)(uintptr_t)(xa ? ga.SA + first * ga.ldsa : ga.SB + e * ga.esb + n0 * ga.ldsb);
+        const uint32_t xlo = __builtin_amdgcn_readfirstlane((uint32_t)xp);  // (to unsigned: no sign is extended)
+        const uint32_t xhi = __builtin_amdgcn_readfirstlane((uint32_t)(xp >> 32));
+        x_base = (const global_u8 *)(((uint64_t)xhi << 32) | xlo);
+        rsa = make_rsrc_u((const void *)(uintptr_t)xp, xa || xb ? (uint32_t)((rows_x - 1) * ldx + ga.KB) : 0u);
     };
     static_assert(!GROUPED || (NW % 2 == 0 && (BM / 8) % 2 == 0), "a wave's A loads are all of one 8-row half");
     auto load_src = [&](int lg) __attribute__((always_inline)) {
@@ -460,6 +480,8 @@ __global__ void __launch_bounds__(64 * WM * WN)
         uint8_t *dst_a = BUF ? s_a1 : s_a0;
         uint8_t *dst_b = BUF ? s_b1 : s_b0;
         const int kb_s = kb_begin + kt * 8;
+        if constexpr (GROUPED && PERSIST && !SVEC)
+            on = on && kb_s < kb_end;
         // K offset of the stage: bytes along a row (row-major), 1 KiB steps
         // (packed B) or 1536-byte steps (dense FP6 A)
         const uint32_t a_k = A6D ? (uint32_t)(kb_s >> 2) * 1536 : (uint32_t)kb_s * 16 * AREG;
@@ -497,7 +519,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
                 off = a_lane + (uint32_t)(rows8 * g.lda_b) + (h ? (uint32_t)((kc1 - kc0) * 16) : 0u);
             if constexpr (AREG > 1)
                 off += (uint32_t)(reg * 128);
-            if constexpr (!SVEC) {  // K tail: blocks at or past the chunk end read as zero
+            if constexpr (!SVEC && !(GROUPED && AFMT == 0)) {  // K tail: blocks at or past the chunk end read as zero
                 // (the K-block chunk kc of the step's tile holds: 8-bit A
                 // chunk kc covers block kc / 2, padded FP6 block kc % 4)
                 const int kc = h ? kc1 : kc0;
@@ -519,8 +541,6 @@ __global__ void __launch_bounds__(64 * WM * WN)
                 off = kn_lane + (uint32_t)(c * KN_RPI) * (uint32_t)g.ldb_b;
             } else if constexpr (GROUPED) {
                 off = b_lane + (uint32_t)(c * 8 * g.ldb_b);
-                if constexpr (!SVEC)
-                    off = kb_s + ((wave & 1) ? kc1 : kc0) < kb_end ? off : kOOB;
             } else {
                 const int rows8 = c * 8, h = c & 1;
                 off = b_lane + (uint32_t)(rows8 * g.ldb_b) + (h ? (uint32_t)((kc1 - kc0) * 16) : 0u);
@@ -543,6 +563,8 @@ __global__ void __launch_bounds__(64 * WM * WN)
 
     ScaleRows sa_rows, sb_rows;
     [[maybe_unused]] v4i x_raw = {0, 0, 0, 0};
+    [[maybe_unused]] uint64_t x_any[2] = {0, 0};
+    [[maybe_unused]] int x_kb = 0;
     uint32_t sbp[SBP_PER_THREAD], sap[SAP_PER_THREAD];
     // dense FP6: this wave's packed scale words of a stage (its 32-row groups
     // of A and of B), one register set per buffer
@@ -562,15 +584,14 @@ __global__ void __launch_bounds__(64 * WM * WN)
             return;
         }
         if constexpr (GROUPED) {
-            // (past the last stage: inside the rows or the range, never used)
-            // SVEC: 16 bytes of the row every other stage, for it and the next
-            if constexpr (SVEC) {
-                if constexpr (BUF == 0)
-                    x_raw = load16(rsa, on ? x_row + kb_s : kOOB);
-            } else {
-                const v2u r = load_scale_row_any(x_base + x_row, kb_s, g.KB);
-                x_raw[0] = (int)r[0];
-                x_raw[1] = (int)r[1];
+            // 16 bytes of the row every other stage, for it and the next (past
+            // the last stage: inside the rows or the range, never used)
+            if constexpr (BUF == 0 && SVEC) {
+                x_raw = load16(rsa, on ? x_row + kb_s : kOOB);
+            } else if constexpr (BUF == 0) {
+                x_any[0] = load_scale_row_any(x_base, x_row, kb_s, g.KB);
+                x_any[1] = load_scale_row_any(x_base, x_row, kb_s + 8, g.KB);
+                x_kb = kb_s;
             }
             return;
         }
@@ -607,8 +628,10 @@ __global__ void __launch_bounds__(64 * WM * WN)
             return;
         uint32_t *dsc = BUF ? s_sc1 : s_sc0;
         if constexpr (GROUPED) {
-            constexpr int H = SVEC && BUF ? 2 : 0;
-            *reinterpret_cast<v2i *>(dsc + tid * 2) = v2i{x_raw[H], x_raw[H + 1]};
+            if constexpr (SVEC)
+                *reinterpret_cast<v2i *>(dsc + tid * 2) = v2i{x_raw[2 * BUF], x_raw[2 * BUF + 1]};
+            else
+                *reinterpret_cast<uint64_t *>(dsc + tid * 2) = scale_row_shift(x_any[BUF], x_kb + 8 * BUF, g.KB);
             return;
         }
         if constexpr (SAPACK) {
@@ -833,7 +856,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
         if (kt < nst)
             stage(kt, B1{}, Rest{}, loadsc);
     };
-    if constexpr (NW == 8 && SVEC) {
+    if constexpr (NW == 8 && (SVEC || GROUPED)) {
         // Eight waves, two per SIMD (waves w and w + 4).  Each stage's
         // prefetch is 64 direct-to-LDS loads per workgroup, which the CU's
         // load path takes about 16 cycles each to accept; a wave whose load

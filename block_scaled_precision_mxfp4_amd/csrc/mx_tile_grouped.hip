@@ -21,8 +21,12 @@ static void launch_tile_grouped(const GroupedTileArgs &g, int64_t grid, hipStrea
 template <int BM, int BN, int WM, int WN, int AFMT>
 static void launch_tile_grouped_persist(const GroupedTileArgs &g, int64_t grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WM, WN, 0, true, false, AFMT, true, false, true>), dim3((unsigned)grid),
-                       dim3(64 * WM * WN), 0, s, g);
+    if (g.scale16)
+        hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WM, WN, 0, true, false, AFMT, true, false, true>), dim3((unsigned)grid),
+                           dim3(64 * WM * WN), 0, s, g);
+    else
+        hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WM, WN, 0, false, false, AFMT, true, false, true>),
+                           dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, g);
 }
 
 // The tiles, largest first, with the mean rows per expert from which each was

@@ -301,7 +301,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     const int64_t grid = ((rows - some) / t.bm + some) * cdiv(N, t.bn);
     g.tiles_n = (int)cdiv(N, t.bn);
     const char *e = std::getenv("MXGEMM_TILE_PERSIST");
-    if (t.persist[bits == 8] && !(e && std::strcmp(e, "0") == 0) && grid > cu && g.scale16 && g.d_stage && N % 8 == 0 &&
+    if (t.persist[bits == 8] && !(e && std::strcmp(e, "0") == 0) && grid > cu && g.d_stage && N % 8 == 0 &&
         groups <= mx::kGroupTable && s.ldd < ((int64_t)1 << 21))
         t.persist[bits == 8](g, cu, stream);
     else
