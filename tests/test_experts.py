@@ -205,6 +205,113 @@ def test_grouped_large(rows, E, N, K, fp8):
     run_grouped(rng, rows, E, N, K, fp8, gather=max(1, rows // 4), cols=np.unique(rng.integers(0, N, 24)), e=(122, 130))
 
 
+TILES = 5  # the grouped product's tiles (indices of MXGEMM_GROUPED_TILE; -1: streaming)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("tile", range(-1, TILES))
+def test_grouped_every_kernel(tile, fp8, monkeypatch):
+    """Each kernel on sizes the plan would give to others: K of 8 blocks, odd block counts, whole pairs of stages; experts
+    without rows, with one and with many; few and many experts."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    rng = np.random.default_rng(50 + tile)
+    for rows, E, N, K, gather in ((7, 3, 40, 256, 0), (300, 5, 264, 288, 90), (333, 4, 130, 512, 0), (290, 70, 72, 480, 33),
+                                  (257, 2, 512, 1056, 300), (400, 130, 48, 1024, 17)):
+        run_grouped(rng, rows, E, N, K, fp8, gather=gather, what="tile %d" % tile)
+    run_grouped(rng, 100, 3, 96, 544, fp8, gather=9, pads=(3, 32, 5, 96, 1), bad_rows=True, odd_scales=True)
+
+
+@pytest.mark.parametrize("K", [512, 800, 1056, 2048])
+def test_grouped_persistent_equals_plain(K, monkeypatch):
+    """The persistent 8-bit tile (more tiles than compute units) against the plain grid, bit for bit, and the oracle: even and
+    odd stage counts, partial tiles, experts without rows, more experts than its table holds."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", "1")
+    for rows, E, N, gather in ((8300, 7, 1096, 700), (5000, 40, 2048, 0), (6000, 1100, 264, 100)):
+        rng = np.random.default_rng(K + rows)
+        off = dev(split_rows(rng, rows, E, "ragged"))
+        a = gather or rows
+        A = dev_u8(inputs.wide_codes(1, a, K, 1))
+        SA, SB = dev_u8(inputs.e8m0_scales(2, a, K, 122, 130)), dev_u8(inputs.e8m0_scales(3, E * N, K, 122, 130))
+        B = dev_u8(inputs.fp4_codes_packed(4, E * N, K))
+        a_rows = dev(rng.integers(0, a, rows).astype(np.int32)) if gather else None
+        got = []
+        for persist in "01":
+            monkeypatch.setenv("MXGEMM_TILE_PERSIST", persist)
+            D = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            say("case grouped persistent", K, rows, E, N, persist)
+            mx.mxgemm_grouped_run(D, A, B, SA, SB, off, rows, N, K, E, a_rows=a_rows, a_count=a, a_format=1)
+            got.append(host_bits(D))
+        assert np.array_equal(got[0], got[1])
+        cols = np.unique(rng.integers(0, N, 9))
+        shape = lambda t: t.cpu().numpy().reshape(E, N, -1)  # noqa: E731
+        r, m, w = ref.grouped(A.cpu().numpy(), SA.cpu().numpy(), shape(B), shape(SB), K, off.cpu().numpy(),
+                              a_rows.cpu().numpy() if gather else None, rows, True, cols=cols)
+        ref.check_grouped(got[0][w][:, cols], r[w], m[w], K, True, "persistent")
+        assert (got[0][~w] == ref.f64_to_bf16(7.0)).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("K", [288, 320, 416, 480])
+def test_grouped_codes_behind_k_add_nothing(K, fp8):
+    """Rows padded with the largest codes and scales of 2^127 behind K: over zeros the product is exactly zero."""
+    rows, N, pad = 80, 200, 128
+    A = torch.full((rows, (K + pad) * (8 if fp8 else 4) // 8), 0x7E if fp8 else 0x77, dtype=torch.uint8, device="cuda")
+    A[:, :K * (8 if fp8 else 4) // 8] = 0
+    B = torch.full((1, N, (K + pad) // 2), 0x77, dtype=torch.uint8, device="cuda")
+    B[:, :, :K // 2] = 0
+    S = torch.full((rows, 24), 0xFE, dtype=torch.uint8, device="cuda")
+    SB = torch.full((1, N, 24), 0xFE, dtype=torch.uint8, device="cuda")
+    D = torch.full((rows, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    say("case grouped codes behind K", K, fp8)
+    mx.mxgemm_grouped_run(D, A, B, S, SB, dev(np.array([0, rows], np.int32)), rows, N, K, 1, a_format=int(fp8), lda=K + pad,
+                          ldb=K + pad, ldsa=24, ldsb=24)
+    assert int(torch.count_nonzero(D)) == 0
+
+
+@pytest.mark.parametrize("tile", [-1, 0, 3])
+def test_grouped_offsets_beyond_32_bits(tile, monkeypatch):
+    """A and D with rows 2^17 bytes and more apart, experts' B 5 GB apart: rows near the end and the second expert."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    rows, N, K, E, lda, ldd = 40000, 24, 256, 2, 1 << 18, 1 << 16
+    rng = np.random.default_rng(4)
+    a, sa = inputs.fp4_codes_packed(1, rows, K), inputs.e8m0_scales(2, rows, K, 120, 130)
+    b, sb = inputs.fp4_codes_packed(3, E * N, K).reshape(E, N, -1), inputs.e8m0_scales(4, E * N, K, 120, 130).reshape(E, N, -1)
+    A = torch.zeros(rows, lda // 2, dtype=torch.uint8, device="cuda")
+    A[:, :K // 2] = dev_u8(a)
+    apart = 5 << 30
+    B = torch.zeros(apart + N * K // 2, dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        B[e * apart:e * apart + N * K // 2] = dev_u8(b[e]).reshape(-1)
+    D = torch.zeros(rows, ldd, dtype=torch.bfloat16, device="cuda")
+    off = np.array([0, 20, rows] if tile < 0 else [0, rows - 70, rows], np.int32)
+    if tile < 0:
+        off[2] = 90
+    say("case grouped 64-bit offsets", tile)
+    mx.mxgemm_grouped_run(D, A, B, dev_u8(sa), dev_u8(sb), dev(off), rows, N, K, E, lda=lda, ldd=ldd, strideb=2 * apart)
+    look = np.unique(np.concatenate([np.arange(90), rng.integers(0, off[2], 60), np.arange(off[2] - 60, off[2])]))
+    look = look[look < off[2]]
+    d = host_bits(D[torch.from_numpy(look).cuda(), :N])
+    r, m, _ = ref.grouped(a, sa, b, sb, K, off, None, rows, False)
+    ref.check_grouped(d, r[look], m[look], K, False)
+
+
+@pytest.mark.parametrize("tile", range(-1, TILES))
+def test_grouped_offsets_that_do_not_ascend_stay_inside(tile, monkeypatch):
+    """What D holds is then not said; what is around D, and rows outside every range, stay as they were."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    rows, N, K = 90, 72, 512
+    for off in ([0, 80, 10, 60], [85, 3, 3, 2], [0, 2 ** 31 - 1, -2 ** 31, 50], [40, 40, 40, 40]):
+        whole = torch.full((rows + 64, N + 16), 11.0, dtype=torch.bfloat16, device="cuda")
+        D = whole[32:32 + rows, 8:]
+        say("case grouped offsets", tile, off)
+        mx.mxgemm_grouped_run(D, dev_u8(inputs.fp4_codes_packed(1, rows, K)), dev_u8(inputs.fp4_codes_packed(2, 3 * N, K)),
+                              dev_u8(inputs.e8m0_scales(3, rows, K, 120, 130)), dev_u8(inputs.e8m0_scales(4, 3 * N, K, 120, 130)),
+                              dev(np.array(off, np.int32)), rows, N, K, 3, ldd=N + 16)
+        torch.cuda.synchronize()
+        assert (whole[:32] == 11).all() and (whole[32 + rows:] == 11).all()
+        assert (whole[:, :8] == 11).all() and (whole[:, 8 + N:] == 11).all()
+
+
 def test_grouped_one_weight_for_all_and_clamped_offsets():
     """strideb = 0 shares one B; offsets outside [0, rows] are clamped."""
     rng = np.random.default_rng(3)
@@ -282,6 +389,27 @@ def test_glu_all_gates_and_specials(fp8):
         bits = np.concatenate([gates.reshape(64, 1024), up.reshape(64, 1024)], 1)
         say("case glu all gates", fp8)
         run_glu(bits, 1024, fp8)
+
+
+def test_glu_and_norm_rows_far_apart():
+    """Row strides of 2 GB and more."""
+    rng = np.random.default_rng(21)
+    K, T, ld = 96, 4, 3 << 29
+    X = torch.zeros(T * ld, dtype=torch.bfloat16, device="cuda")
+    rows = X.as_strided((T, 2 * K), (ld, 1))
+    bits = bf16_bits(rng, T, 2 * K)
+    rows.copy_(dev_bf16(bits))
+    A, S = torch.zeros(T, K, dtype=torch.uint8, device="cuda"), torch.zeros(T, K // 32, dtype=torch.uint8, device="cuda")
+    say("case glu far rows")
+    mx.mxgemm_glu_quantize(A, S, X, T, K, ldx=ld, a_format=1)
+    a, s = ref.quantize(ref.glu(bits, K), True)
+    assert np.array_equal(A.cpu().numpy(), a) and np.array_equal(S.cpu().numpy(), s)
+    H = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    w = bf16_bits(rng, K)
+    say("case norm far rows")
+    mx.mxgemm_norm_quantize(T, K, X, X=X[K:], H=H, w_post=dev_bf16(w), ldy=ld, ldx=ld, res_scale=0.5)
+    h, _ = ref.norm(bits[:, :K], K, X=bits[:, K:], w_post=w, res_scale=0.5)
+    assert np.array_equal(host_bits(H), h)
 
 
 @pytest.mark.parametrize("live", [-3, 0, 5, 99])
@@ -498,6 +626,24 @@ def test_block_on_another_stream():
     b.run(stream=s)
     s.synchronize()
     assert equal(eager, b.outputs())
+
+
+def test_two_blocks_at_once():
+    """Two blocks on two streams without an order between them, each as alone."""
+    blocks = [Block(60, 8, 2, 256, 128, 3, False), Block(33, 16, 4, 256, 96, 6, True)]
+    want = []
+    for i, b in enumerate(blocks):
+        b.feed(i)
+        b.run()
+        want.append(b.outputs())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    say("case two blocks at once")
+    for _ in range(5):
+        for b, s in zip(blocks, streams):
+            b.run(stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(blocks, want):
+        assert equal(w, b.outputs())
 
 
 def test_two_captured_blocks_replay():
