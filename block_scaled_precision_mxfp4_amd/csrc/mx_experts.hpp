@@ -59,7 +59,7 @@ struct NormArgs {
     float res_scale, eps;
     int fp8;
 };
-void launch_norm(const NormArgs &n, hipStream_t s);
+void launch_norm(const NormArgs &n, int num_cu, hipStream_t s);
 
 // ---- product grouped by expert
 // The tiled kernel's arguments (mx_tile.hip: GemmArgs with M = rows of D, no

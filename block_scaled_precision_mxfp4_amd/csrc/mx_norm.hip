@@ -206,16 +206,21 @@ static void launch_norm_as(const NormArgs &n, hipStream_t s)
         hipLaunchKernelGGL((mx_norm_kernel<NT, C, false>), dim3((unsigned)n.T), dim3(NT), 0, s, n);
 }
 
-void launch_norm(const NormArgs &n, hipStream_t s)
+// Up to one token per compute unit a workgroup twice as wide, 8 elements a
+// thread: its latency is what counts (1 x 4096, top 4: 4.6 against 5.6 us). For
+// more tokens 16 a thread (8192 x 4096: 96.9 us with top 4, 5.2 TB/s, and 58.3
+// without, against 101.4 and 64.8 us; 32 a thread: 124.6 and 73.7).
+void launch_norm(const NormArgs &n, int num_cu, hipStream_t s)
 {
+    const bool wide = n.T <= num_cu;
     if (n.K <= 512)
         launch_norm_as<64, 1>(n, s);
     else if (n.K <= 2048)
         launch_norm_as<256, 1>(n, s);
     else if (n.K <= 4096)
-        launch_norm_as<256, 2>(n, s);
+        wide ? launch_norm_as<512, 1>(n, s) : launch_norm_as<256, 2>(n, s);
     else if (n.K <= 8192)
-        launch_norm_as<512, 2>(n, s);
+        wide ? launch_norm_as<1024, 1>(n, s) : launch_norm_as<512, 2>(n, s);
     else
         launch_norm_as<1024, 2>(n, s);
 }

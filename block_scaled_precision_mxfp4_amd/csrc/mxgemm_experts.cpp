@@ -196,7 +196,8 @@ mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream
             return MXGEMM_ERR_ALIGN;
     if (!aligned(n->pos, 4) || !aligned(n->weights, 4))
         return MXGEMM_ERR_ALIGN;
-    const mxgemm_status st = mx::check_device();
+    int cu = 0;
+    const mxgemm_status st = mx::check_device(&cu);
     if (st != MXGEMM_OK)
         return st;
     mx::NormArgs a;
@@ -225,7 +226,7 @@ mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream
     a.res_scale = n->res_scale;
     a.eps = n->eps;
     a.fp8 = bits == 8;
-    mx::launch_norm(a, stream);
+    mx::launch_norm(a, cu, stream);
     return launched();
 }
 

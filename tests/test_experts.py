@@ -58,7 +58,7 @@ def check_route(x, k, renorm, got):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 32, 4), (3, 5, 5), (63, 16, 2), (64, 33, 16), (65, 64, 6), (200, 100, 7),
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 32, 4), (3, 5, 5), (63, 16, 2), (64, 33, 16), (65, 64, 6), (200, 100, 7), (1000, 24, 3),
                                    (130, 128, 8), (129, 256, 3), (70, 257, 16), (67, 1000, 9), (300, 1024, 1), (2050, 2, 1)])
 def test_route(T, E, k, bf16):
     rng = np.random.default_rng(T * 1031 + E * 7 + k)
@@ -488,6 +488,13 @@ def test_norm(T, K, fp8):
     rng = np.random.default_rng(T * 31 + K)
     run_norm(rng, T, K, fp8, top_k=4)
     run_norm(rng, T, K, fp8, top_k=0, gate="rows", pad=8)
+
+
+@pytest.mark.parametrize("K", [512, 2048, 2080, 4096, 4160, 8192, 8224])
+def test_norm_of_more_tokens_than_compute_units(K):
+    rng = np.random.default_rng(K)
+    run_norm(rng, 300, K, True, top_k=2)
+    run_norm(rng, 300, K, False, gate="rows")
 
 
 @pytest.mark.parametrize("opts", [dict(post=False), dict(pre=False), dict(x=False, gate="one"), dict(h=False, z=False),
