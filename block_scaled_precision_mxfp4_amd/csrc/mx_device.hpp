@@ -370,19 +370,6 @@ __device__ __forceinline__ void atomic_add_quad(const Epilogue &ep, int m, int n
     }
 }
 
-// A butterfly's partner inside 16 lanes by row permutes (no LDS): steps 0..3
-// are lane ^ 1, lane ^ 2, the mirrored lane of 8 and of 16 (whose quads and
-// halves already agree).
-__device__ __forceinline__ uint32_t row_partner(uint32_t v, int step)
-{
-    switch (step) {
-    case 0: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
-    case 1: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
-    case 2: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);
-    default: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);
-    }
-}
-
 // Map a hardware workgroup id to a logical one so that the workgroups the
 // dispatcher sends to the same XCD (ids congruent mod 8) receive
 // consecutive logical ids, i.e. neighbouring output tiles sharing operand

@@ -7,8 +7,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "mx_args.hpp"
-
 namespace mx {
 
 // ---- router choice (mx_route.hip)
@@ -62,17 +60,25 @@ struct NormArgs {
 void launch_norm(const NormArgs &n, int num_cu, hipStream_t s);
 
 // ---- product grouped by expert
-// The tiled kernel's arguments (mx_tile.hip: GemmArgs with M = rows of D, no
-// C, unsplit, row-major operands) and what the groups add.
-struct GroupedTileArgs : GemmArgs {
+struct GroupedArgs {
+    uint16_t *D;             // bf16 [M][ldd]
+    const uint8_t *A, *B;    // [a_count][lda_b] FP4 or FP8, [E][N][ldb_b] FP4 (byte pitches)
+    const uint8_t *SA, *SB;  // E8M0 [a_count][ldsa], [E][N][ldsb]
     const int32_t *offsets;  // [E + 1]
     const int32_t *a_rows;   // [M] or null
-    int a_count, E;
+    float alpha;
+    int M, a_count, N, K, E;
+    int KB;                  // K / 32 scale blocks
+    int64_t ldd, lda_b, ldsa, ldb_b, ldsb;
     int64_t eb_b, esb;       // bytes from one expert's B, and scales, to the next's
+    int tiles_n;             // column tiles
+    int group_m;             // an expert's row tiles whose column tiles are taken together
+    int d_vec, d_stage;      // 8-byte stores to D allowed; 16-byte ones
+    int scale16;             // whole 16-block groups of scale bytes, rows 16-byte aligned
 };
 // Experts that the persistent tiled kernel keeps a table of in LDS.
 constexpr int kGroupTable = 1024;
-typedef void (*GroupedLaunchFn)(const GroupedTileArgs &, int64_t grid, hipStream_t);
+typedef void (*GroupedLaunchFn)(const GroupedArgs &, int64_t grid, hipStream_t);
 struct GroupedTileKernel {
     int bm, bn;
     int min_rows[2];             // rows per expert from which it is taken: FP4 A, FP8 E4M3 A
@@ -81,6 +87,6 @@ struct GroupedTileKernel {
 };
 const GroupedTileKernel *grouped_tile_kernels(int *count);
 // Few rows per expert (mx_grouped.hip)
-void launch_grouped_stream(bool fp8, const GroupedTileArgs &g, hipStream_t s);
+void launch_grouped_stream(bool fp8, const GroupedArgs &g, hipStream_t s);
 
 }  // namespace mx

@@ -11,7 +11,7 @@
 // element, each once.  Four lanes share a block and hold 8 elements each.
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
-#include "mx_quantize.hpp"
+#include "mx_quantize_out.hpp"
 
 namespace mx {
 

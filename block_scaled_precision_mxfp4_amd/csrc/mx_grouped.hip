@@ -19,7 +19,7 @@
 namespace mx {
 
 template <bool FP8, bool SVEC, int KS, int DEPTH>
-__global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedTileArgs g)
+__global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
 {
     using a_t = typename std::conditional<FP8, v8i, v4i>::type;
     constexpr int AKB = FP8 ? 32 : 16;  // bytes of an A K-block
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedTileArgs 
 constexpr int kStreamKs = 2, kStreamDepth = 2;
 
 template <bool FP8>
-static void launch_stream_as(const GroupedTileArgs &g, hipStream_t s)
+static void launch_stream_as(const GroupedArgs &g, hipStream_t s)
 {
     constexpr int R = 64 / kStreamKs;  // rows of B per workgroup
     const dim3 grid((unsigned)((g.N + R - 1) / R), (unsigned)(g.E < g.M ? g.E : g.M));
@@ -146,7 +146,7 @@ static void launch_stream_as(const GroupedTileArgs &g, hipStream_t s)
         hipLaunchKernelGGL((mx_grouped_stream_kernel<FP8, false, kStreamKs, kStreamDepth>), grid, dim3(256), 0, s, g);
 }
 
-void launch_grouped_stream(bool fp8, const GroupedTileArgs &g, hipStream_t s)
+void launch_grouped_stream(bool fp8, const GroupedArgs &g, hipStream_t s)
 {
     if (fp8)
         launch_stream_as<true>(g, s);

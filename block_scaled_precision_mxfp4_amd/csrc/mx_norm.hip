@@ -18,7 +18,8 @@
 // written per element with every output asked for.
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
-#include "mx_quantize.hpp"
+#include "mx_quantize_out.hpp"
+#include "mx_rows16.hpp"
 
 namespace mx {
 

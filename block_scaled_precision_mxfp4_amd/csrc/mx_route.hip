@@ -22,6 +22,7 @@
 // Bound by latency (and for long inputs by reading the logits).
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
+#include "mx_rows16.hpp"
 
 namespace mx {
 

@@ -9,7 +9,6 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "mx_args.hpp"
 #include "mx_experts.hpp"
 #include "mx_host.hpp"
 
@@ -249,7 +248,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     if (s.lda % 2 || s.ldb % 2 || s.strideb % 2 || !aligned(A, 16) || !aligned(B, 16) || (s.lda * bits) % 128 ||
         (s.ldb / 2) % 16 || (s.strideb / 2) % 16 || !aligned(D, 2) || !aligned(offsets, 4) || !aligned(a_rows, 4))
         return MXGEMM_ERR_ALIGN;
-    mx::GroupedTileArgs g = {};
+    mx::GroupedArgs g = {};
     g.lda_b = s.lda * bits / 8;
     g.ldb_b = s.ldb / 2;
     // the kernels address a tile's rows of B, and through a row list all of
@@ -277,7 +276,6 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     g.ldsb = s.ldsb;
     g.eb_b = s.strideb / 2;
     g.esb = s.strideb_scale;
-    g.split = 1;
     g.d_vec = aligned(D, 8) && s.ldd % 4 == 0;
     g.d_stage = aligned(D, 16) && s.ldd % 8 == 0;
     auto scale_rows = [&](const void *p, int64_t ld, int64_t n) { return g.KB % n == 0 && aligned(p, n) && ld % n == 0; };
