@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     uint32_t a_row[A_CH / NW], x_row = 0;      // byte offsets of A's rows (with the chunk) and of the scale row
     const uint8_t *a_base = nullptr, *b_base = nullptr;
     const global_u8 *x_base = nullptr;
+    bool x_in = false;                         // the scale row is there
     uint32_t a_bytes = 0, b_bytes = 0;
     __amdgpu_buffer_rsrc_t rsx = make_rsrc(nullptr, 0);
     // chunk of lane l in the wave's 8-row half (the rows' swizzle)
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         const int u = xa ? tid : tid - XA * 64;
         const int rows_x = xa ? rows_a : rows_b;
         const int64_t ldx = xa ? g.ldsa : g.ldsb;
-        const bool x_in = (xa ? u < BM : xb && u < BN) && (uint32_t)raw_x < (uint32_t)rows_x;
+        x_in = (xa ? u < BM : xb && u < BN) && (uint32_t)raw_x < (uint32_t)rows_x;
         x_row = x_in ? (uint32_t)(raw_x * ldx) : SVEC ? kFar : 0u;
         const uint64_t xp = (uint64_t)(uintptr_t)(xa ? g.SA + first * g.ldsa : g.SB + e * g.esb + n0 * g.ldsb);
         const uint32_t xlo = __builtin_amdgcn_readfirstlane((uint32_t)xp);  // (to unsigned: no sign is extended)
@@ -217,7 +218,10 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
                 s_total = total;
         }
         __syncthreads();
-        units = __builtin_amdgcn_readfirstlane(s_total) * g.tiles_n;
+        // (no more than rows can make when the offsets ascend: what they hold
+        // does not decide how long this runs)
+        const int some = min(g.E, g.M);
+        units = min(__builtin_amdgcn_readfirstlane(s_total), (g.M - some) / BM + some) * g.tiles_n;
         if (unit >= units)
             return;
     }
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         if constexpr (SVEC)
             *reinterpret_cast<v2i *>(dst) = v2i{x_raw[2 * BUF], x_raw[2 * BUF + 1]};
         else
-            *reinterpret_cast<uint64_t *>(dst) = scale_row_shift(x_any[BUF], x_kb + 8 * BUF, g.KB);
+            *reinterpret_cast<uint64_t *>(dst) = x_in ? scale_row_shift(x_any[BUF], x_kb + 8 * BUF, g.KB) : 0;
     };
 
     // LDS byte offset of this lane's 16 bytes of a fragment inside its 16-row

@@ -113,8 +113,11 @@ def split_rows(rng, rows, E, kind):
     return cut.astype(np.int32)
 
 
+TILES = 5  # the grouped product's tiles (indices of MXGEMM_GROUPED_TILE; -1: streaming)
+
+
 def run_grouped(rng, rows, E, N, K, fp8, kind="ragged", gather=0, alpha=1.0, pads=(0, 0, 0, 0, 0), e=(118, 132),
-                bad_rows=False, cols=None, odd_scales=False, what="", special_scales=False):
+                bad_rows=False, nan_first=False, cols=None, odd_scales=False, what="", special_scales=False):
     """pads: of ldd, lda, ldsa, ldb, ldsb (elements or bytes)."""
     a_count = gather if gather else rows
     bits = 8 if fp8 else 4
@@ -132,6 +135,8 @@ def run_grouped(rng, rows, E, N, K, fp8, kind="ragged", gather=0, alpha=1.0, pad
     if special_scales:
         SA[rng.integers(0, a_count, 2), rng.integers(0, KB)] = 0xFF
         SB[rng.integers(0, E), rng.integers(0, N, 2), rng.integers(0, KB)] = 0xFF
+    if nan_first:
+        SA[0] = 0xFF
     off = split_rows(rng, rows, E, kind)
     a_rows = rng.integers(0, a_count, rows).astype(np.int32) if gather else None
     if bad_rows:
@@ -192,6 +197,20 @@ def test_grouped_strides_and_bad_rows(rows, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("K", [512, 544])
+@pytest.mark.parametrize("tile", range(-1, TILES))
+def test_grouped_rows_that_are_not_there_are_zeros_beside_a_nan_row(tile, K, fp8, monkeypatch):
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    run_grouped(np.random.default_rng(K + tile), 150, 3, 144, K, fp8, gather=40, bad_rows=True, nan_first=True, what="nan first")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("kind", ["ragged", "one"])
+def test_grouped_many_rows_of_a_short_k(kind, fp8):
+    run_grouped(np.random.default_rng(5), 700, 4, 80, 96, fp8, kind=kind, gather=300, what="short K")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
 @pytest.mark.parametrize("rows", [9, 400])
 def test_grouped_special_scales(rows, fp8):
     rng = np.random.default_rng(rows)
@@ -203,9 +222,6 @@ def test_grouped_special_scales(rows, fp8):
 def test_grouped_large(rows, E, N, K, fp8):
     rng = np.random.default_rng(rows)
     run_grouped(rng, rows, E, N, K, fp8, gather=max(1, rows // 4), cols=np.unique(rng.integers(0, N, 24)), e=(122, 130))
-
-
-TILES = 5  # the grouped product's tiles (indices of MXGEMM_GROUPED_TILE; -1: streaming)
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
@@ -422,7 +438,7 @@ def test_glu_live_rows_are_clamped(live):
 # ---- norms ------------------------------------------------------------------------
 
 def run_norm(rng, T, K, fp8, top_k=0, post=True, gate=None, x=True, pre=True, h=True, z=True, q=True, pad=0, scale=0.75,
-             sigma=1.0, missing=0.2, alias=False, y=None):
+             sigma=1.0, missing=0.2, alias=False, y=None, nan_first=False):
     y_rows = T * max(top_k, 1) + (3 if top_k else 0)
     Y = bf16_bits(rng, y_rows, K, sigma=sigma) if y is None else y
     kw, dk = {}, {}
@@ -431,6 +447,8 @@ def run_norm(rng, T, K, fp8, top_k=0, post=True, gate=None, x=True, pre=True, h=
         p = np.full((bits.shape[0], K + pad), 0x7FC0, np.uint16)
         p[:, :K] = bits
         return dev_bf16(p)
+    if top_k and nan_first:
+        Y[0] = 0x7FC0  # (no token's row)
     if top_k:
         pos = rng.permutation(y_rows)[:T * top_k].reshape(T, top_k).astype(np.int32)
         pos[rng.random((T, top_k)) < missing] = -1
@@ -438,6 +456,9 @@ def run_norm(rng, T, K, fp8, top_k=0, post=True, gate=None, x=True, pre=True, h=
         if T > 1:
             pos[1] = -1  # a token that no expert took
         weights = rng.random((T, top_k)).astype(np.float32)
+        if nan_first:
+            pos[pos == 0] = -1
+            weights[(pos < 0) | (pos >= y_rows)] = np.nan
         kw.update(pos=pos, weights=weights)
         dk.update(pos=dev(pos), weights=dev(weights), top_k=top_k, y_rows=y_rows)
     if post:
@@ -506,6 +527,12 @@ def test_norm_options(opts):
     for T, K in ((9, 320), (3, 4096)):
         run_norm(rng, T, K, True, **opts)
         run_norm(rng, T, K, False, **opts)
+
+
+def test_norm_absent_rows_add_nothing_whatever_stands_there():
+    rng = np.random.default_rng(13)
+    for T, K, k in ((5, 320, 3), (3, 4096, 4), (300, 2080, 5)):
+        run_norm(rng, T, K, True, top_k=k, nan_first=True)
 
 
 def test_norm_zeros_and_specials():
