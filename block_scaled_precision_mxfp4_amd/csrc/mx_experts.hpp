@@ -57,6 +57,7 @@ struct NormArgs {
     float res_scale, eps;
     int fp8;
 };
+int norm_threads(int K);  // a workgroup's, one per token (twice as many with few tokens)
 void launch_norm(const NormArgs &n, int num_cu, hipStream_t s);
 
 // ---- product grouped by expert

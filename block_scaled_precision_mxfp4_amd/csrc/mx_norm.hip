@@ -207,6 +207,8 @@ static void launch_norm_as(const NormArgs &n, hipStream_t s)
         hipLaunchKernelGGL((mx_norm_kernel<NT, C, false>), dim3((unsigned)n.T), dim3(NT), 0, s, n);
 }
 
+int norm_threads(int K) { return K <= 512 ? 64 : K <= 4096 ? 256 : K <= 8192 ? 512 : 1024; }
+
 // Up to one token per compute unit a workgroup twice as wide, 8 elements a
 // thread: its latency is what counts (1 x 4096, top 4: 4.6 against 5.6 us). For
 // more tokens 16 a thread (8192 x 4096: 96.9 us with top 4, 5.2 TB/s, and 58.3

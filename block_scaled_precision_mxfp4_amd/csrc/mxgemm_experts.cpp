@@ -15,7 +15,8 @@
 namespace {
 
 constexpr int kMaxK = 1 << 24;
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of a launch, exclusive
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -102,7 +103,7 @@ mxgemm_status mxgemm_route(int32_t *ids, float *weights, int32_t *pos, int32_t *
         (renorm != 0 && renorm != 1))
         return MXGEMM_ERR_INVALID_ARG;
     if (T < 1 || E < 1 || E > mx::kRouteMaxExperts || top_k < 1 || top_k > mx::kRouteMaxTopK || top_k > E || ldl < E ||
-        (int64_t)T * top_k > kMaxGrid)
+        (int64_t)T * top_k > kMaxInt)
         return MXGEMM_ERR_SHAPE;
     if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(pos, 4) || !aligned(offsets, 4) || !aligned(rows, 4) ||
         !aligned(logits, bf16 ? 2 : 4))
@@ -151,7 +152,7 @@ mxgemm_status mxgemm_glu_quantize(void *A, void *scaleA, const void *X, const in
     if (!aligned(X, 16) || ldx % 8 || !aligned(live, 4))
         return MXGEMM_ERR_ALIGN;
     const int64_t blocks = (int64_t)M * (K / 32);
-    if (mx::glu_grid(blocks) > kMaxGrid)
+    if (mx::glu_grid(blocks) * 256 >= kMaxThreads)
         return MXGEMM_ERR_SHAPE;
     st = mx::check_device();
     if (st != MXGEMM_OK)
@@ -181,7 +182,7 @@ mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream
     if (!bits)
         return MXGEMM_ERR_INVALID_ARG;
     if (T < 1 || K < 32 || K % 32 || K > mx::kNormMaxK || n->ldy < K || (n->top_k > 0 && n->y_rows < 1) ||
-        (n->X && n->ldx < K) || (n->gate && n->ldg != 0 && n->ldg < K) || (n->H && n->ldh < K) || (n->Z && n->ldz < K))
+        (int64_t)T * mx::norm_threads(K) >= kMaxThreads || (n->X && n->ldx < K) || (n->gate && n->ldg != 0 && n->ldg < K) || (n->H && n->ldh < K) || (n->Z && n->ldz < K))
         return MXGEMM_ERR_SHAPE;
     if (n->A) {
         const mxgemm_status st = check_quantized(n->A, K, n->lda, n->ldsa, bits);
@@ -282,15 +283,14 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     g.scale16 = scale_rows(scaleA, s.ldsa, 16) && scale_rows(scaleB, s.ldsb, 16) && s.strideb_scale % 16 == 0;
     g.group_m = 8;
 
-    // (every launch below is within the grid limit: rows and N are)
-    if (((int64_t)rows / 32 + std::min(rows, groups) + 1) * cdiv(N, 32) > kMaxGrid)
-        return MXGEMM_ERR_SHAPE;
     int cu = 0;
     const mxgemm_status st = mx::check_device(&cu);
     if (st != MXGEMM_OK)
         return st;
     const int kernel = plan_grouped(rows, N, K, groups, bits, cu);
     if (kernel < 0) {
+        if (cdiv(N, 32) * 256 >= kMaxThreads)
+            return MXGEMM_ERR_SHAPE;
         mx::launch_grouped_stream(bits == 8, g, stream);
         return launched();
     }
@@ -298,6 +298,8 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     const mx::GroupedTileKernel &t = mx::grouped_tile_kernels(&n_tiles)[kernel];
     const int64_t some = std::min(rows, groups);
     const int64_t grid = ((rows - some) / t.bm + some) * cdiv(N, t.bn);
+    if (grid * 512 >= kMaxThreads)  // (a tile's threads are 512 at most)
+        return MXGEMM_ERR_SHAPE;
     g.tiles_n = (int)cdiv(N, t.bn);
     const char *e = std::getenv("MXGEMM_TILE_PERSIST");
     if (t.persist[bits == 8] && !(e && std::strcmp(e, "0") == 0) && grid > cu && g.d_stage && N % 8 == 0 &&

@@ -487,8 +487,9 @@ typedef struct mxgemm_grouped {
  * rows]), and a row index outside [0, a_count) reads as a row of zeros.
  *
  * Shapes: rows, a_count, N >= 1; 1 <= groups <= 65535; K >= 32, K % 32 == 0,
- * K <= 2^24; 256 rows of B and of a scale matrix, and with a row list all of
- * A and of scaleA, below 2^31 bytes (else MXGEMM_ERR_SHAPE).  Alignment: A, B
+ * K <= 2^24; 256 rows of A, of B and of a scale matrix, and with a row list all
+ * of A and of scaleA, below 2^31 bytes; fewer than 2^23 tiles, the smallest of
+ * 32 x 128 elements of D (else MXGEMM_ERR_SHAPE).  Alignment: A, B
  * 16-byte aligned, the byte pitches of A, B and strideb multiples of 16; D 2
  * bytes, offsets and a_rows 4 bytes.  D must not overlap an input.
  * Asynchronous on `stream`; errors as mxgemm_run.
@@ -511,7 +512,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
  *
  * live: NULL, or a device int32 (offsets + groups, say): only rows below *live
  * (clamped to [0, M]) are read and written.  Shapes: M >= 1, K >= 32, K % 32
- * == 0, K <= 2^24, ldx >= 2K.  X 16-byte aligned, ldx % 8 == 0; live 4-byte
+ * == 0, K <= 2^24, M * K < 2^35, ldx >= 2K.  X 16-byte aligned, ldx % 8 == 0; live 4-byte
  * aligned.  X must not overlap the outputs.  Asynchronous on `stream`.
  */
 mxgemm_status mxgemm_glu_quantize(void *A, void *scaleA, const void *X, const int32_t *live, int M, int K, int64_t ldx,
@@ -528,8 +529,8 @@ mxgemm_status mxgemm_glu_quantize(void *A, void *scaleA, const void *X, const in
  * to H (the residual stream), Z and, quantized, A with scaleA; each of the
  * three may be NULL, not all.  The arithmetic between the bf16 inputs and the
  * two roundings is in 64 bits.  pos entries outside [0, y_rows) add nothing
- * (mxgemm_route's -1; Y is not read for them): a token that no expert took
- * has y = 0.
+ * (mxgemm_route's -1), whatever their weights and Y hold: a token that no
+ * expert took has y = 0.
  */
 typedef struct mxgemm_norm {
     const void *Y;        /* bf16 [y_rows][ldy] (top_k > 0) or [T][ldy] */
@@ -558,7 +559,8 @@ typedef struct mxgemm_norm {
 
 /*
  * T >= 1 tokens of K elements, K % 32 == 0, 32 <= K <= 16384 (a token is kept
- * in one workgroup's registers).  bf16 pointers 16-byte aligned, their
+ * in one workgroup's registers), T below 2^22 (K <= 512: 2^26, K <= 4096:
+ * 2^24, K <= 8192: 2^23).  bf16 pointers 16-byte aligned, their
  * strides multiples of 8; A as in mxgemm_glu_quantize.  Apart from the places
  * named above no output overlaps an input or another output.  Errors:
  * MXGEMM_ERR_INVALID_ARG (NULL n or Y, no output, A without scaleA or the
