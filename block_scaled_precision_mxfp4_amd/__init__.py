@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxgemm.so")
@@ -71,6 +72,7 @@ class Info(ctypes.Structure):
         return d
 
 
+# (the two structs below are passed packed: a fifth of a Structure's time)
 class Grouped(ctypes.Structure):
     _fields_ = [("ldd", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64), ("ldb", ctypes.c_int64),
                 ("ldsb", ctypes.c_int64), ("strideb", ctypes.c_int64), ("strideb_scale", ctypes.c_int64),
@@ -86,6 +88,9 @@ class Norm(ctypes.Structure):
                 ("scaleA", ctypes.c_void_p), ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64),
                 ("a_format", ctypes.c_int32)]
 
+
+_pack_grouped = struct.Struct("@7qi4x").pack
+_pack_norm = struct.Struct("@PqPPiiPPqPqffPqPPqPPqqi4x").pack
 
 _lib = None
 
@@ -125,11 +130,11 @@ def lib():
         L.mxgemm_route_workspace_bytes.argtypes = [i32, i32]
         L.mxgemm_route_workspace_bytes.restype = ctypes.c_size_t
         L.mxgemm_grouped_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, i32, i32, i32, i32,
-                                         ctypes.POINTER(Grouped), vp]
+                                         ctypes.c_char_p, vp]
         L.mxgemm_grouped_run.restype = i32
         L.mxgemm_glu_quantize.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i64, i32, vp]
         L.mxgemm_glu_quantize.restype = i32
-        L.mxgemm_norm_quantize.argtypes = [ctypes.POINTER(Norm), i32, i32, vp]
+        L.mxgemm_norm_quantize.argtypes = [ctypes.c_char_p, i32, i32, vp]
         L.mxgemm_norm_quantize.restype = i32
         L.mxgemm_query.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
         L.mxgemm_query.restype = i32
@@ -155,11 +160,7 @@ def _status_text(status):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def _stream(stream):
@@ -312,11 +313,11 @@ def mxgemm_grouped_run(D, A, B, scaleA, scaleB, offsets, rows, N, K, groups, a_r
     KB = K // 32
     ldb = K if ldb is None else ldb
     ldsb = KB if ldsb is None else ldsb
-    g = Grouped(N if ldd is None else ldd, K if lda is None else lda, KB if ldsa is None else ldsa, ldb, ldsb,
-                N * ldb if strideb is None else strideb, N * ldsb if strideb_scale is None else strideb_scale, a_format)
+    g = _pack_grouped(N if ldd is None else ldd, K if lda is None else lda, KB if ldsa is None else ldsa, ldb, ldsb,
+                      N * ldb if strideb is None else strideb, N * ldsb if strideb_scale is None else strideb_scale, a_format)
     st = lib().mxgemm_grouped_run(_ptr(D), _ptr(A), _ptr(B), _ptr(scaleA), _ptr(scaleB), _ptr(offsets), _ptr(a_rows),
                                   float(alpha), int(rows), int(rows if a_count is None else a_count), int(N), int(K),
-                                  int(groups), ctypes.byref(g), _stream(stream))
+                                  int(groups), g, _stream(stream))
     if check:
         _check(st, "mxgemm_grouped_run")
     return st
@@ -340,11 +341,12 @@ def mxgemm_norm_quantize(T, K, Y, X=None, H=None, Z=None, A=None, scaleA=None, p
     """Weighted sum of a token's rows of Y, norm, gate, residual -> H; its
     norm -> Z and, quantized, A and scaleA (asynchronous; strides default to
     dense rows; a gate of one row for all tokens: ldg=0)."""
-    ld = [K if v is None else v for v in (ldy, ldg, ldx, ldh, ldz, lda)]
-    n = Norm(_ptr(Y), ld[0], _ptr(pos), _ptr(weights), top_k, y_rows, _ptr(w_post), _ptr(gate), ld[1], _ptr(X), ld[2],
-             res_scale, eps, _ptr(H), ld[3], _ptr(w_pre), _ptr(Z), ld[4], _ptr(A), _ptr(scaleA), ld[5],
-             K // 32 if ldsa is None else ldsa, a_format)
-    st = lib().mxgemm_norm_quantize(ctypes.byref(n), int(T), int(K), _stream(stream))
+    n = _pack_norm(_ptr(Y) or 0, K if ldy is None else ldy, _ptr(pos) or 0, _ptr(weights) or 0, top_k, y_rows,
+                   _ptr(w_post) or 0, _ptr(gate) or 0, K if ldg is None else ldg, _ptr(X) or 0, K if ldx is None else ldx,
+                   res_scale, eps, _ptr(H) or 0, K if ldh is None else ldh, _ptr(w_pre) or 0, _ptr(Z) or 0,
+                   K if ldz is None else ldz, _ptr(A) or 0, _ptr(scaleA) or 0, K if lda is None else lda,
+                   K // 32 if ldsa is None else ldsa, a_format)
+    st = lib().mxgemm_norm_quantize(n, int(T), int(K), _stream(stream))
     if check:
         _check(st, "mxgemm_norm_quantize")
     return st

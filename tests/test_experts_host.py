@@ -45,6 +45,13 @@ def test_struct_layouts_match_the_header():
     assert got == want
 
 
+def test_packed_structs_are_the_structs():
+    rng = np.random.default_rng(1)
+    for pack, cls in ((mx._pack_grouped, mx.Grouped), (mx._pack_norm, mx.Norm)):
+        v = [float(np.float32(rng.random())) if t is ctypes.c_float else int(rng.integers(1, 1 << 30)) for _, t in cls._fields_]
+        assert pack(*v) == bytes(cls(*v))
+
+
 def _route(**kw):
     a = dict(ids=0x1000, weights=0x2000, pos=0x3000, offsets=0x4000, rows=0x5000, logits=0x6000, T=64, E=32, top_k=4,
              workspace=None, workspace_bytes=0, stream=0)
