@@ -84,7 +84,7 @@ struct GroupedTileKernel {
     int bm, bn;
     int min_rows[2];             // rows per expert from which it is taken: FP4 A, FP8 E4M3 A
     GroupedLaunchFn launch[2];   // FP4 A, FP8 E4M3 A (may be null)
-    GroupedLaunchFn persist[2];  // persistent (may be null): 16-byte rows of D, N % 8 == 0, at most kGroupTable experts
+    GroupedLaunchFn persist[2];  // persistent (may be null): 16-byte rows of D, N % 8 == 0, K >= 256, at most kGroupTable experts
 };
 const GroupedTileKernel *grouped_tile_kernels(int *count);
 // Few rows per expert (mx_grouped.hip)

@@ -59,12 +59,22 @@ namespace mx {
 typedef __attribute__((address_space(1))) uint8_t global_u8;
 
 // A row's scale bytes of 8 K-blocks from kb on at any alignment: one load that
-// ends at the row's end (KB >= 8 blocks) at the latest, to be shifted by
-// scale_row_shift.  base is wave-uniform, row the lane's offset.
+// ends at the row's end at the latest, to be shifted by scale_row_shift.  base
+// is wave-uniform, row the lane's offset.
 __device__ __forceinline__ uint64_t load_scale_row_any(const global_u8 *base, uint32_t row, int kb, int KB)
 {
     typedef uint64_t __attribute__((aligned(1))) any_u64;
-    return *reinterpret_cast<const __attribute__((address_space(1))) any_u64 *>(base + min(kb, KB - 8) + row);
+    return *reinterpret_cast<const __attribute__((address_space(1))) any_u64 *>(base + max(min(kb, KB - 8), 0) + row);
+}
+
+// ... of a whole row of fewer than 8 blocks, byte by byte, as if the load
+// had begun 8 - KB bytes before it.
+__device__ __forceinline__ uint64_t load_scale_row_short(const global_u8 *base, uint32_t row, int KB)
+{
+    uint64_t w = 0;
+    for (int i = 0; i < KB; ++i)
+        w |= (uint64_t)base[row + i] << (8 * (8 - KB + i));
+    return w;
 }
 
 // ... to block kb's byte first and zeros for blocks at or past KB.
@@ -370,7 +380,15 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     };
 
     issue_operands(0, true, B0{});
-    issue_scales(0, true, B0{});
+    if (!SVEC && !PERSIST && g.KB < 8) {
+        // one stage: the one that its prefetch asks for, which is not used,
+        // would read before or behind a row (there are at least two offsets)
+        x_any[0] = load_scale_row_short(x_base, x_row, g.KB);
+        x_base = (const global_u8 *)(uintptr_t)g.offsets;
+        x_row = 0;
+    } else {
+        issue_scales(0, true, B0{});
+    }
     wait_vmcnt<0>();
     commit_scales(B0{});
     __syncthreads();

@@ -60,12 +60,10 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     (8 experts of 128 rows, N = 2048, K = 4096, FP8: 21.1 us on 91 % of them
 //     with 64 x 128, 26.3 us on half of them with 128 x 256).
 // MXGEMM_GROUPED_TILE=<index> (-1: streaming) is the tests' choice instead.
-int plan_grouped(int rows, int N, int K, int groups, int bits, int num_cu)
+int plan_grouped(int rows, int N, int groups, int bits, int num_cu)
 {
     int n_tiles = 0;
     const mx::GroupedTileKernel *tiles = mx::grouped_tile_kernels(&n_tiles);
-    if (K < 256)  // (the tiled kernel reads scale rows 8 bytes at a time)
-        return -1;
     if (const char *e = std::getenv("MXGEMM_GROUPED_TILE")) {
         const int k = std::atoi(e);
         if (k < n_tiles && (k < 0 || tiles[k].launch[bits == 8]))
@@ -287,7 +285,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     const mxgemm_status st = mx::check_device(&cu);
     if (st != MXGEMM_OK)
         return st;
-    const int kernel = plan_grouped(rows, N, K, groups, bits, cu);
+    const int kernel = plan_grouped(rows, N, groups, bits, cu);
     if (kernel < 0) {
         if (cdiv(N, 32) * 256 >= kMaxThreads)
             return MXGEMM_ERR_SHAPE;
@@ -303,7 +301,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     g.tiles_n = (int)cdiv(N, t.bn);
     const char *e = std::getenv("MXGEMM_TILE_PERSIST");
     if (t.persist[bits == 8] && !(e && std::strcmp(e, "0") == 0) && grid > cu && g.d_stage && N % 8 == 0 &&
-        groups <= mx::kGroupTable && s.ldd < ((int64_t)1 << 21))
+        K >= 256 && groups <= mx::kGroupTable && s.ldd < ((int64_t)1 << 21))
         t.persist[bits == 8](g, cu, stream);
     else
         t.launch[bits == 8](g, grid, stream);

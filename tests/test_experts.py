@@ -211,6 +211,15 @@ def test_grouped_many_rows_of_a_short_k(kind, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("K", [32, 96, 128, 224, 256])
+@pytest.mark.parametrize("tile", range(-1, TILES))
+def test_grouped_short_k_of_every_kernel(tile, K, fp8, monkeypatch):
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    run_grouped(np.random.default_rng(K), 300, 3, 136, K, fp8, gather=40, bad_rows=True, nan_first=True, what="short K")
+    run_grouped(np.random.default_rng(K), 33, 2, 70, K, fp8, pads=(1, 32, 3, 32, 5), what="short K")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
 @pytest.mark.parametrize("rows", [9, 400])
 def test_grouped_special_scales(rows, fp8):
     rng = np.random.default_rng(rows)
