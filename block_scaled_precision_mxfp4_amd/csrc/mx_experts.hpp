@@ -13,6 +13,8 @@ namespace mx {
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 16;
 constexpr int kRouteUnit = 64;        // tokens whose slots are ranked together
+constexpr int kRouteFew = 16;         // ... of up to kRouteFewTokens tokens in more than one workgroup
+constexpr int kRouteFewTokens = 4096;
 constexpr int kRouteMaxBlocks = 256;  // workgroups of the selection; each takes whole units
 struct RouteArgs {
     const void *logits;  // f32 or bf16 [T][ldl]
@@ -21,11 +23,12 @@ struct RouteArgs {
     int32_t *pos;        // [T][k]
     int32_t *offsets;    // [E + 1]
     int32_t *rows;       // [T * k]
-    int32_t *counts;     // workspace [blocks][E] (blocks > 1)
+    void *counts;        // workspace [blocks][E] (blocks > 1): uint8 with kRouteFew, else int32
     int T, E, k;
     int64_t ldl;
     int bf16, renorm;
-    int units;           // 64-token units per workgroup
+    int unit;            // tokens ranked together: kRouteUnit or kRouteFew
+    int units;           // units per workgroup
     int blocks;
 };
 void launch_route(const RouteArgs &r, hipStream_t s);

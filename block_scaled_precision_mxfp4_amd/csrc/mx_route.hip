@@ -10,21 +10,27 @@
 // Weights are exp(x - max) / sum in fp32, the sum over the chosen experts or
 // over all of them.
 //
-// Grouping, without atomics, so that the order is that of the tokens.  64
-// tokens' slots are ranked together: for 64 consecutive slots a wave finds
+// Grouping, without atomics, so that the order is that of the tokens.  A
+// unit's slots, those of 64 tokens, are ranked together: for 64 consecutive slots a wave finds
 // the lanes with the same expert from one ballot per bit of the expert's
 // number; the rank inside the wave is a population count, and a count per
 // (wave, expert) in LDS, summed over the waves in order, makes it the rank
-// inside the 64 tokens.  With one workgroup (T <= 64) the offsets follow in
-// the same launch; otherwise every workgroup leaves its counts in the
-// workspace and a second kernel adds the counts of the workgroups before it.
+// inside the unit.  With one workgroup (T <= 64) the offsets follow in the
+// same launch; otherwise every workgroup leaves its counts in the workspace and
+// a second kernel adds the counts of the workgroups before it.  From 65 to
+// 4096 tokens a unit is 16 tokens: four times as many compute units share the
+// rounds, and counts of a byte keep the second launch's reads as they were
+// (64-token units against 16, both launches, us: 509 tokens of 64 experts, top
+// 6, 8.1 / 7.1; 1024 of 128, top 8, 10.4 / 8.5; 4096 of 512 63 / 32; 4096 of 128
+// 11.3 / 11.4; at 2048 of 256, top 2, they lose, 10.0 / 10.7).
 //
-// Bound by latency: one token of 32 experts, top 4, 3.9 us; 509 of 64, top 6, 5.7
-// and 3.8 us for the two launches.  Long inputs: 16384 tokens of 128 experts, top
-// 8 (8.4 MB of logits, 1.6 us at the copy's rate), 10.2 us in the selection's
-// rounds, about 60 instructions each, and 7.0 us in the second launch, whose
-// every workgroup reads all workgroups' counts (4 units a workgroup there, for
-// a quarter of these reads: 10.0 us).
+// Bound by latency: one token of 32 experts, top 4, 3.9 us (waves without a token
+// skip the rounds: 4.2 without that, 1 token of 1024 experts 53 -> 22).  Long
+// inputs: 16384 tokens of 128 experts, top 8 (8.4 MB of logits, 1.6 us at the
+// copy's rate), 14.6 us: the selection's rounds, about 60 instructions each,
+// then the second launch, whose every workgroup reads all workgroups' counts (4
+// units a workgroup there, for a quarter of these reads: 7.0 -> 10.0 us; 16 or
+// 32 reads in flight instead of 8: no gain).
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
 #include "mx_rows16.hpp"
@@ -92,36 +98,44 @@ __device__ __forceinline__ void exclusive_scan(const int *count, int *start, int
         start[E] = carry;
 }
 
-// V: experts per lane (E <= 16 V); NT: threads (16 NT-lane tokens a pass)
-template <int V, int NT, bool BF16>
+// V: experts per lane (E <= 16 V); NT: threads (NT / 16 tokens a pass); TOK:
+// tokens ranked together
+template <int V, int NT, bool BF16, int TOK>
 __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
 {
     constexpr int NW = NT / 64;
     constexpr int TPP = NT / 16;                     // tokens per pass
-    constexpr int CPW = kRouteMaxTopK / NW > 0 ? kRouteMaxTopK / NW : 1;  // 64-slot chunks per wave
+    constexpr int MAXCH = TOK * kRouteMaxTopK / 64;
+    constexpr int CPW = MAXCH / NW > 0 ? MAXCH / NW : 1;  // 64-slot chunks per wave
     extern __shared__ int s_mem[];
     int *s_base = s_mem;                             // [E + 1] rows of this workgroup per expert so far
     int *s_start = s_mem + r.E + 1;                  // [E + 1]
-    int16_t *s_id = reinterpret_cast<int16_t *>(s_start + r.E + 1);  // [64 k]
-    uint16_t *s_cnt = reinterpret_cast<uint16_t *>(s_id + kRouteUnit * kRouteMaxTopK);  // [k][E]
+    int16_t *s_id = reinterpret_cast<int16_t *>(s_start + r.E + 1);  // [TOK k]
+    uint16_t *s_cnt = reinterpret_cast<uint16_t *>(s_id + TOK * kRouteMaxTopK);  // [chunks][E]
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l = lane & 15;
     const int k = r.k, E = r.E;
+    const int chunks = (TOK * k + 63) / 64;
     for (int e = tid; e < E; e += NT)
         s_base[e] = 0;
 
     for (int unit = 0; unit < r.units; ++unit) {
-        const int64_t t0 = ((int64_t)blockIdx.x * r.units + unit) * kRouteUnit;
+        const int64_t t0 = ((int64_t)blockIdx.x * r.units + unit) * TOK;
         if (t0 >= r.T)
             break;
-        for (int i = tid; i < k * E; i += NT)
+        for (int i = tid; i < chunks * E; i += NT)
             s_cnt[i] = 0;
 #pragma unroll 1
-        for (int pass = 0; pass < kRouteUnit / TPP; ++pass) {
+        for (int pass = 0; pass < TOK / TPP; ++pass) {
             const int u = pass * TPP + tid / 16;  // token of the unit
             const int64_t t = t0 + u;
             const bool live = t < r.T;
+            if (t0 + pass * TPP + wave * 4 >= r.T) {  // (none of the wave's four)
+                if (l < k)
+                    s_id[u * k + l] = -1;
+                continue;
+            }
             uint32_t key[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -187,8 +201,9 @@ __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
             const int c = i * NW + wave;
             rank[i] = 0;
             id[i] = -1;
-            if (c < k) {
-                id[i] = s_id[c * 64 + lane];
+            if (c < chunks) {
+                if (TOK == 64 || c * 64 + lane < TOK * k)
+                    id[i] = s_id[c * 64 + lane];
                 uint64_t same = __ballot(id[i] >= 0);
                 for (int b = 0; (1 << b) < E; ++b) {
                     const bool bit = (id[i] >> b) & 1;
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
         __syncthreads();
         for (int e = tid; e < E; e += NT) {
             int run = 0;
-            for (int c = 0; c < k; ++c) {
+            for (int c = 0; c < chunks; ++c) {
                 const int n = s_cnt[c * E + e];
                 s_cnt[c * E + e] = (uint16_t)run;
                 run += n;
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
         for (int i = 0; i < CPW; ++i) {
             const int c = i * NW + wave;
             const int64_t slot = t0 * k + c * 64 + lane;
-            if (c < k && slot < (int64_t)r.T * k)
+            if (c * 64 + lane < TOK * k && slot < (int64_t)r.T * k)
                 r.pos[slot] = id[i] >= 0 ? s_base[id[i]] + s_cnt[c * E + id[i]] + rank[i] : -1;
         }
         __syncthreads();
@@ -226,8 +241,12 @@ __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
     }
 
     if (r.blocks > 1) {
-        for (int e = tid; e < E; e += NT)
-            r.counts[(int64_t)blockIdx.x * E + e] = s_base[e];
+        for (int e = tid; e < E; e += NT) {
+            if constexpr (TOK == kRouteFew)  // (one unit: 16 at most)
+                reinterpret_cast<uint8_t *>(r.counts)[(int64_t)blockIdx.x * E + e] = (uint8_t)s_base[e];
+            else
+                reinterpret_cast<int32_t *>(r.counts)[(int64_t)blockIdx.x * E + e] = s_base[e];
+        }
         return;
     }
     // one workgroup, one unit: the ranks are final, the offsets follow
@@ -257,6 +276,7 @@ __global__ void __launch_bounds__(NT) mx_route_select_kernel(RouteArgs r)
 }
 
 // Second launch: workgroup b's ranks become positions.
+template <typename Count>
 __global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
 {
     extern __shared__ int s_mem[];
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int b = b0 + i * (1024 / ep);
-                c[i] = b < r.blocks ? r.counts[(int64_t)b * E + e] : 0;
+                c[i] = b < r.blocks ? (int)reinterpret_cast<const Count *>(r.counts)[(int64_t)b * E + e] : 0;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -298,8 +318,8 @@ __global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
         for (int i = tid; i <= E; i += 1024)
             r.offsets[i] = s_start[i];
     const int64_t slots = (int64_t)r.T * k;
-    const int64_t first = (int64_t)blockIdx.x * r.units * kRouteUnit * k;
-    const int64_t last = min(slots, first + (int64_t)r.units * kRouteUnit * k);
+    const int64_t first = (int64_t)blockIdx.x * r.units * r.unit * k;
+    const int64_t last = min(slots, first + (int64_t)r.units * r.unit * k);
     for (int64_t i = first + tid; i < last; i += 1024) {
         const int id = r.ids[i];
         if (id >= 0) {
@@ -312,19 +332,28 @@ __global__ void __launch_bounds__(1024) mx_route_place_kernel(RouteArgs r)
     }
 }
 
+template <int V, int NT, int TOK>
+static void launch_select_unit(const RouteArgs &r, hipStream_t s)
+{
+    const size_t lds = (size_t)(2 * (r.E + 1)) * 4 + TOK * kRouteMaxTopK * 2 + (size_t)((TOK * r.k + 63) / 64) * r.E * 2;
+    if (r.bf16)
+        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, true, TOK>), dim3(r.blocks), dim3(NT), lds, s, r);
+    else
+        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, false, TOK>), dim3(r.blocks), dim3(NT), lds, s, r);
+}
+
 template <int V, int NT>
 static void launch_select(const RouteArgs &r, hipStream_t s)
 {
-    const size_t lds = (size_t)(2 * (r.E + 1)) * 4 + kRouteUnit * kRouteMaxTopK * 2 + (size_t)r.k * r.E * 2;
-    if (r.bf16)
-        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, true>), dim3(r.blocks), dim3(NT), lds, s, r);
+    if (r.unit == kRouteFew)
+        launch_select_unit<V, 16 * kRouteFew, kRouteFew>(r, s);
     else
-        hipLaunchKernelGGL((mx_route_select_kernel<V, NT, false>), dim3(r.blocks), dim3(NT), lds, s, r);
+        launch_select_unit<V, NT, kRouteUnit>(r, s);
 }
 
 void launch_route(const RouteArgs &r, hipStream_t s)
 {
-    // 64 tokens a pass where a lane's keys leave room for 16 waves
+    // 64 tokens a pass where a lane's keys leave room for 16 waves, 32 for 8
     if (r.E <= 32)
         launch_select<2, 1024>(r, s);
     else if (r.E <= 64)
@@ -333,10 +362,14 @@ void launch_route(const RouteArgs &r, hipStream_t s)
         launch_select<8, 1024>(r, s);
     else if (r.E <= 256)
         launch_select<16, 1024>(r, s);
+    else if (r.E <= 512)
+        launch_select<32, 512>(r, s);
     else
         launch_select<64, 256>(r, s);
-    if (r.blocks > 1)
-        hipLaunchKernelGGL(mx_route_place_kernel, dim3(r.blocks), dim3(1024), (size_t)(3 * r.E + 1) * 4, s, r);
+    if (r.blocks > 1 && r.unit == kRouteFew)
+        hipLaunchKernelGGL(mx_route_place_kernel<uint8_t>, dim3(r.blocks), dim3(1024), (size_t)(3 * r.E + 1) * 4, s, r);
+    else if (r.blocks > 1)
+        hipLaunchKernelGGL(mx_route_place_kernel<int32_t>, dim3(r.blocks), dim3(1024), (size_t)(3 * r.E + 1) * 4, s, r);
 }
 
 }  // namespace mx

@@ -38,15 +38,11 @@ mxgemm_status check_quantized(const void *A, int K, int64_t lda, int64_t ldsa, i
 
 mxgemm_status launched() { return hipGetLastError() == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP; }
 
-int route_units(int T) { return (int)(((int64_t)T + mx::kRouteUnit - 1) / mx::kRouteUnit); }
-int route_units_per_block(int T) { return (route_units(T) + mx::kRouteMaxBlocks - 1) / mx::kRouteMaxBlocks; }
-int route_blocks(int T)
-{
-    const int per = route_units_per_block(T);
-    return (route_units(T) + per - 1) / per;
-}
-
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Units of the selection per workgroup, and its workgroups
+int route_units_per_block(int T, int unit) { return (int)cdiv(cdiv(T, unit), mx::kRouteMaxBlocks); }
+int route_blocks(int T, int unit) { return (int)cdiv(cdiv(T, unit), route_units_per_block(T, unit)); }
 
 // The grouped product's kernel: an index into the tiles, or -1 for streaming.
 // The host knows the rows and experts, not how the rows are spread.
@@ -89,7 +85,9 @@ size_t mxgemm_route_workspace_bytes(int T, int E)
 {
     if (T < 1 || E < 1 || E > mx::kRouteMaxExperts)
         return 0;
-    const int blocks = route_blocks(T);
+    // (room for four times as many workgroups of kRouteFew tokens, whose
+    // counts are a byte each)
+    const int blocks = route_blocks(T, mx::kRouteUnit);
     return blocks > 1 ? (size_t)blocks * E * 4 : 0;
 }
 
@@ -123,15 +121,16 @@ mxgemm_status mxgemm_route(int32_t *ids, float *weights, int32_t *pos, int32_t *
     r.pos = pos;
     r.offsets = offsets;
     r.rows = rows;
-    r.counts = (int32_t *)workspace;
+    r.counts = workspace;
     r.T = T;
     r.E = E;
     r.k = top_k;
     r.ldl = ldl;
     r.bf16 = bf16;
     r.renorm = renorm;
-    r.units = route_units_per_block(T);
-    r.blocks = route_blocks(T);
+    r.unit = T > mx::kRouteUnit && T <= mx::kRouteFewTokens ? mx::kRouteFew : mx::kRouteUnit;
+    r.units = route_units_per_block(T, r.unit);
+    r.blocks = route_blocks(T, r.unit);
     mx::launch_route(r, stream);
     return launched();
 }

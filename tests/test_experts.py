@@ -70,6 +70,14 @@ def test_route(T, E, k, bf16):
         check_route(x.astype(np.float64), k, renorm, run_route(x, k, renorm, bf16, ldl=E + 3))
 
 
+@pytest.mark.parametrize("T", [65, 80, 4096, 4097])
+@pytest.mark.parametrize("E,k", [(7, 3), (40, 8), (100, 5), (200, 1), (384, 8), (700, 16)])
+def test_route_units_and_expert_counts(T, E, k):
+    x = np.random.default_rng(T * 7 + E).standard_normal((T, E)).astype(np.float32)
+    say("case route", T, E, k)
+    check_route(x.astype(np.float64), k, True, run_route(x, k, True, False))
+
+
 def test_route_more_than_one_unit_a_workgroup():
     T, E, k = 64 * 256 + 100, 8, 2
     x = np.random.default_rng(5).standard_normal((T, E)).astype(np.float32)
