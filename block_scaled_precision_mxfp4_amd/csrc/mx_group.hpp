@@ -5,6 +5,7 @@
 #pragma once
 
 #include "mx_device.hpp"
+#include "mx_rows16.hpp"
 
 namespace mx {
 
@@ -43,17 +44,6 @@ struct GroupTile {
     int tn;      // column tile
 };
 
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v, int lane)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        v += lane >= d ? o : 0;
-    }
-    return v;
-}
-
 // Tile lg of all, in an expert with rows first .. end - 1 whose last row tile
 // is number upto - 1.
 __device__ __forceinline__ bool tile_in_group(int lg, int first, int end, int upto, int bm, int tiles_n, int group_m,
@@ -83,7 +73,7 @@ __device__ __forceinline__ bool group_tile(const int32_t *offsets, int E, int ro
     int lo = 0, hi = 0, upto = 0;  // of the last 64 experts looked at
     for (int e0 = 0; e0 < E; e0 += 64) {
         group_range(offsets, E, rows, e0 + lane, lo, hi);
-        upto = total + wave_scan((max(hi - lo, 0) + bm - 1) / bm, lane);
+        upto = total + wave_scan((max(hi - lo, 0) + bm - 1) / bm);
         total = __builtin_amdgcn_readlane(upto, 63);
     }
     if (wg >= total * tiles_n)
@@ -94,7 +84,7 @@ __device__ __forceinline__ bool group_tile(const int32_t *offsets, int E, int ro
         int before = 0;
         for (int e0 = 0;; e0 += 64) {
             group_range(offsets, E, rows, e0 + lane, lo, hi);
-            upto = before + wave_scan((max(hi - lo, 0) + bm - 1) / bm, lane);
+            upto = before + wave_scan((max(hi - lo, 0) + bm - 1) / bm);
             const int last = __builtin_amdgcn_readlane(upto, 63);
             if (want < last || e0 + 64 >= E) {
                 t.e = e0;
@@ -121,7 +111,7 @@ __device__ __forceinline__ int make_group_table(const int32_t *offsets, int E, i
     for (int e0 = 0; e0 < E; e0 += 64) {
         int lo, hi;
         group_range(offsets, E, rows, e0 + lane, lo, hi);
-        const int upto = total + wave_scan((max(hi - lo, 0) + bm - 1) / bm, lane);
+        const int upto = total + wave_scan((max(hi - lo, 0) + bm - 1) / bm);
         total = __builtin_amdgcn_readlane(upto, 63);
         if (e0 + lane < E) {
             s_lo[e0 + lane] = lo;

@@ -84,15 +84,10 @@ __device__ __forceinline__ void exclusive_scan(const int *count, int *start, int
     for (int e0 = 0; e0 < E; e0 += 64) {
         const int e = e0 + lane;
         const int c = e < E ? count[e] : 0;
-        int s = c;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(s, d);
-            s += lane >= d ? o : 0;
-        }
+        const int s = wave_scan(c);
         if (e < E)
             start[e] = carry + s - c;
-        carry += __shfl(s, 63);
+        carry += __builtin_amdgcn_readlane(s, 63);
     }
     if (lane == 0)
         start[E] = carry;

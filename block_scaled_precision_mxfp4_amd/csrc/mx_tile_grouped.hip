@@ -171,8 +171,16 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     // multiplies zeros)
     const int nst = PERSIST ? (g.KB + 15) / 16 * 2 : (g.KB + 7) / 8;
 
+    // rows of the tile: of A's load i, and of the thread's scales (A's or B's)
+    auto a_tile_row = [&](int i) __attribute__((always_inline)) { return ((i * NW + wave) % (BM / 8)) * 8 + (lane >> 3); };
+    const int x_tile_row = wave < XA ? tid : tid - XA * 64;
     // first part: expert, rows and columns, and the row list's values, which
-    // are used in the second one, after whatever hides their latency
+    // are used in the second one, after whatever hides their latency.  Rows
+    // past the expert's end are -1: the plain form reads its last row's number
+    // for them and drops it in row_of, because a condition here makes each
+    // load wait (45.0 -> 43.8 us for 2036 rows of 64 experts, N = 1440, K =
+    // 2880); in the persistent form, whose wait is hidden, the condition here is
+    // the faster one (279 against 284 us, the shape below)
     auto find_tile = [&](int wg, int total) __attribute__((always_inline)) {
         GroupTile gt;
         if constexpr (PERSIST) {
@@ -186,34 +194,47 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         m0 = __builtin_amdgcn_readfirstlane(gt.m0);
         m_end = __builtin_amdgcn_readfirstlane(gt.m1);
         n0 = __builtin_amdgcn_readfirstlane(gt.tn) * BN;
-        auto read = [&](int r) __attribute__((always_inline)) {
-            return m0 + r < m_end ? (g.a_rows ? g.a_rows[m0 + r] : r) : -1;
-        };
+        if constexpr (PERSIST) {
+            auto read = [&](int r) __attribute__((always_inline)) {
+                return m0 + r < m_end ? (g.a_rows ? g.a_rows[m0 + r] : r) : -1;
+            };
 #pragma unroll
-        for (int i = 0; i < A_CH / NW; ++i)
-            raw_a[i] = read(((i * NW + wave) % (BM / 8)) * 8 + (lane >> 3));
-        const int u = wave < XA ? tid : tid - XA * 64;  // row of the wave's operand
-        raw_x = wave < XA && u < BM ? read(u) : u;
+            for (int i = 0; i < A_CH / NW; ++i)
+                raw_a[i] = read(a_tile_row(i));
+            raw_x = wave < XA && x_tile_row < BM ? read(x_tile_row) : -1;
+        } else if (g.a_rows) {
+#pragma unroll
+            for (int i = 0; i < A_CH / NW; ++i)
+                raw_a[i] = g.a_rows[min(m0 + a_tile_row(i), m_end - 1)];
+            raw_x = g.a_rows[min(m0 + x_tile_row, m_end - 1)];
+        }
         return true;
     };
-    auto set_tile = [&]() __attribute__((always_inline)) {
+    auto row_of = [&](int r, int raw) __attribute__((always_inline)) {
+        return PERSIST ? raw : m0 + r < m_end ? (g.a_rows ? raw : r) : -1;
+    };
+    auto set_tile_b = [&]() __attribute__((always_inline)) {
+        b_base = g.B + e * g.eb_b + n0 * g.ldb_b;
+        b_bytes = (uint32_t)((min(BN, g.N - n0) - 1) * g.ldb_b + (int64_t)g.KB * 16);
+    };
+    auto set_tile_a = [&]() __attribute__((always_inline)) {
         // without a row list the tile's own rows, from its first one on
         const int64_t first = g.a_rows ? 0 : m0;
         const int rows_a = g.a_rows ? g.a_count : min(BM, m_end - m0);
         const int rows_b = min(BN, g.N - n0);
 #pragma unroll
-        for (int i = 0; i < A_CH / NW; ++i)
-            a_row[i] = (uint32_t)raw_a[i] < (uint32_t)rows_a ? (uint32_t)(raw_a[i] * g.lda_b) + (uint32_t)(kc_lane * 16) : kFar;
+        for (int i = 0; i < A_CH / NW; ++i) {
+            const int r = row_of(a_tile_row(i), raw_a[i]);
+            a_row[i] = (uint32_t)r < (uint32_t)rows_a ? (uint32_t)(r * g.lda_b) + (uint32_t)(kc_lane * 16) : kFar;
+        }
         a_base = g.A + first * g.lda_b;
         a_bytes = (uint32_t)((rows_a - 1) * g.lda_b + (int64_t)g.KB * 16 * AREG);
-        b_base = g.B + e * g.eb_b + n0 * g.ldb_b;
-        b_bytes = (uint32_t)((rows_b - 1) * g.ldb_b + (int64_t)g.KB * 16);
         const bool xa = wave < XA, xb = !xa && wave < XA + XB;
-        const int u = xa ? tid : tid - XA * 64;
+        const int r = xa ? row_of(x_tile_row, raw_x) : x_tile_row;
         const int rows_x = xa ? rows_a : rows_b;
         const int64_t ldx = xa ? g.ldsa : g.ldsb;
-        x_in = (xa ? u < BM : xb && u < BN) && (uint32_t)raw_x < (uint32_t)rows_x;
-        x_row = x_in ? (uint32_t)(raw_x * ldx) : SVEC ? kFar : 0u;
+        x_in = (xa ? x_tile_row < BM : xb && x_tile_row < BN) && (uint32_t)r < (uint32_t)rows_x;
+        x_row = x_in ? (uint32_t)(r * ldx) : SVEC ? kFar : 0u;
         const uint64_t xp = (uint64_t)(uintptr_t)(xa ? g.SA + first * g.ldsa : g.SB + e * g.esb + n0 * g.ldsb);
         const uint32_t xlo = __builtin_amdgcn_readfirstlane((uint32_t)xp);  // (to unsigned: no sign is extended)
         const uint32_t xhi = __builtin_amdgcn_readfirstlane((uint32_t)(xp >> 32));
@@ -237,13 +258,12 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     }
     if (!find_tile(unit, units))
         return;
-    set_tile();
 
     // ---- stage loaders.  Per stage the base advances along K and the range
     // shrinks by the same amount; a stage that must not load gets an empty
     // range: every load returns zeros without traffic.
-    auto issue_operands = [&](int kt, bool on, auto bufc) __attribute__((always_inline)) {
-        constexpr int BUF = decltype(bufc)::value;
+    auto issue_operands = [&](int kt, bool on, auto bufc, auto whichc) __attribute__((always_inline)) {
+        constexpr int BUF = decltype(bufc)::value, WHICH = decltype(whichc)::value;  // WHICH: 1 A, 2 B, 3 both
         uint8_t *dst_a = BUF ? s_a1 : s_a0;
         uint8_t *dst_b = BUF ? s_b1 : s_b0;
         const int kb_s = kt * 8;
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         const auto ra = make_rsrc(a_base + a_k, on ? a_bytes - a_k : 0u);
         const auto rb = make_rsrc(b_base + b_k, on ? b_bytes - b_k : 0u);
 #pragma unroll
-        for (int i = 0; i < A_CH / NW; ++i) {
+        for (int i = 0; i < (WHICH & 1 ? A_CH / NW : 0); ++i) {
             const int c = i * NW + wave;
             uint32_t off = a_row[i];
             if constexpr (FP8) {
@@ -265,7 +285,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
             load16_to_lds(ra, (lds_void *)(dst_a + c * 1024), off);
         }
 #pragma unroll
-        for (int i = 0; i < B_CH / NW; ++i) {
+        for (int i = 0; i < (WHICH & 2 ? B_CH / NW : 0); ++i) {
             const int c = i * NW + wave;
             load16_to_lds(rb, (lds_void *)(dst_b + c * 1024), b_lane + (uint32_t)(c * 8 * g.ldb_b));
         }
@@ -308,6 +328,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     v4f acc[FN][FM];
     using B0 = std::integral_constant<int, 0>;
     using B1 = std::integral_constant<int, 1>;
+    using Both = std::integral_constant<int, 3>;
 
     // One stage: prefetch stage kt+1 into the other buffer, multiply stage kt,
     // then wait for the prefetch and publish its scales.  LOADS_AT places the
@@ -322,7 +343,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         auto prefetch = [&]() __attribute__((always_inline)) {
             if constexpr (LOADS_AT >= 0)
                 __builtin_amdgcn_sched_barrier(0);
-            issue_operands(kt + 1, more, Next{});
+            issue_operands(kt + 1, more, Next{}, Both{});
             issue_scales(kt + 1, more, Next{});
             if constexpr (LOADS_AT >= 0)
                 __builtin_amdgcn_sched_barrier(0);
@@ -379,7 +400,12 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         __syncthreads();
     };
 
-    issue_operands(0, true, B0{});
+    // (B first: the row list is still under way)
+    set_tile_b();
+    if constexpr (!PERSIST)
+        issue_operands(0, true, B0{}, std::integral_constant<int, 2>{});
+    set_tile_a();
+    issue_operands(0, true, B0{}, std::integral_constant<int, PERSIST ? 3 : 1>{});
     if (!SVEC && !PERSIST && g.KB < 8) {
         // one stage: the one that its prefetch asks for, which is not used,
         // would read before or behind a row (there are at least two offsets)
@@ -427,8 +453,9 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
         if (next_found) {
             // the next tile's first stage into buffer 0 (its last readers
             // passed the barrier ending stage nst - 2)
-            set_tile();
-            issue_operands(0, true, B0{});
+            set_tile_b();
+            set_tile_a();
+            issue_operands(0, true, B0{}, Both{});
             issue_scales(0, true, B0{});
         }
         // D through the last stage's A buffer, 1/PARTS of the wave tile at a
