@@ -24,10 +24,10 @@
 // 6, 8.1 / 7.1; 1024 of 128, top 8, 10.4 / 8.5; 4096 of 512 63 / 32; 4096 of 128
 // 11.3 / 11.4; at 2048 of 256, top 2, they lose, 10.0 / 10.7).
 //
-// Bound by latency: one token of 32 experts, top 4, 3.9 us (waves without a token
-// skip the rounds: 4.2 without that, 1 token of 1024 experts 53 -> 22).  Long
+// Bound by latency: one token of 32 experts, top 4, 3.6 us (waves without a token
+// skip the rounds: 0.3 less, 1 token of 1024 experts 53 -> 22).  Long
 // inputs: 16384 tokens of 128 experts, top 8 (8.4 MB of logits, 1.6 us at the
-// copy's rate), 14.6 us: the selection's rounds, about 60 instructions each,
+// copy's rate), 14.0 us: the selection's rounds, about 60 instructions each,
 // then the second launch, whose every workgroup reads all workgroups' counts (4
 // units a workgroup there, for a quarter of these reads: 7.0 -> 10.0 us; 16 or
 // 32 reads in flight instead of 8: no gain).

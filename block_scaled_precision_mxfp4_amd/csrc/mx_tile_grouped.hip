@@ -41,7 +41,7 @@
 // us; the FP4 256 x 256 tile has no registers left for it (13 spilled, 207 ->
 // 212 us).
 //
-// Bound (FP4, 256 x 256, the shape above: 194-208 us, 2.6-2.8 PFLOP/s): a stage
+// Bound (FP4, 256 x 256, the shape above: 195-203 us, 2.7-2.8 PFLOP/s): a stage
 // takes about 4300 cycles of which 2048 are matrix instructions, as in the
 // dense kernel on row-major operands (181 us for the same flops in one group;
 // 156 us with packed ones); partly filled tiles are 12 % of the work.
