@@ -16,6 +16,8 @@ namespace {
 
 constexpr int kMaxK = 1 << 24;
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int kMaxRows = 1 << 30;                  // of a grouped product: a tile past them still counts in an int
+constexpr int kMaxSum = 1024;                      // rows that a token's weighted sum adds
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of a launch, exclusive
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -178,7 +180,7 @@ mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream
     const int bits = elem_bits(n->a_format);
     if (!bits)
         return MXGEMM_ERR_INVALID_ARG;
-    if (T < 1 || K < 32 || K % 32 || K > mx::kNormMaxK || n->ldy < K || (n->top_k > 0 && n->y_rows < 1) ||
+    if (T < 1 || n->top_k > kMaxSum || K < 32 || K % 32 || K > mx::kNormMaxK || n->ldy < K || (n->top_k > 0 && n->y_rows < 1) ||
         (int64_t)T * mx::norm_threads(K) >= kMaxThreads || (n->X && n->ldx < K) || (n->gate && n->ldg != 0 && n->ldg < K) || (n->H && n->ldh < K) || (n->Z && n->ldz < K))
         return MXGEMM_ERR_SHAPE;
     if (n->A) {
@@ -239,7 +241,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
     const int bits = elem_bits(s.a_format);
     if (!bits)
         return MXGEMM_ERR_INVALID_ARG;
-    if (rows < 1 || a_count < 1 || (!a_rows && a_count < rows) || N < 1 || K < 32 || K % 32 || K > kMaxK || groups < 1 ||
+    if (rows < 1 || rows > kMaxRows || a_count < 1 || (!a_rows && a_count < rows) || N < 1 || K < 32 || K % 32 || K > kMaxK || groups < 1 ||
         groups > 65535 || s.ldd < N || s.lda < K || s.ldsa < K / 32 || s.ldb < K || s.ldsb < K / 32 || s.strideb < 0 ||
         s.strideb_scale < 0)
         return MXGEMM_ERR_SHAPE;

@@ -486,7 +486,7 @@ typedef struct mxgemm_grouped {
  * hold, no address outside the buffers is formed (they are clamped to [0,
  * rows]), and a row index outside [0, a_count) reads as a row of zeros.
  *
- * Shapes: rows, a_count, N >= 1; 1 <= groups <= 65535; K >= 32, K % 32 == 0,
+ * Shapes: rows, a_count, N >= 1; rows <= 2^30; 1 <= groups <= 65535; K >= 32, K % 32 == 0,
  * K <= 2^24; 256 rows of A, of B and of a scale matrix, and with a row list all
  * of A and of scaleA, below 2^31 bytes; fewer than 2^23 tiles, the smallest of
  * 32 x 128 elements of D (else MXGEMM_ERR_SHAPE).  Alignment: A, B
@@ -537,7 +537,7 @@ typedef struct mxgemm_norm {
     int64_t ldy;
     const int32_t *pos;   /* [T][top_k], dense; NULL with top_k == 0 */
     const float *weights; /* [T][top_k], dense; NULL with top_k == 0 */
-    int32_t top_k;        /* rows of Y summed per token; 0: row t of Y itself */
+    int32_t top_k;        /* rows of Y summed per token, at most 1024; 0: row t of Y itself */
     int32_t y_rows;       /* rows of Y (used with top_k > 0) */
     const void *w_post;   /* bf16 [K] or NULL */
     const void *gate;     /* bf16 [T][ldg], or one row for all with ldg == 0; NULL: 1 */

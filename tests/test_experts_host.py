@@ -92,7 +92,7 @@ def _grouped(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(D=None), -1), (dict(A=None), -1), (dict(B=None), -1), (dict(scaleA=None), -1), (dict(scaleB=None), -1),
     (dict(offsets=None), -1), (dict(a_format=2), -1), (dict(a_format=3), -1), (dict(a_format=-1), -1),
-    (dict(rows=0), -2), (dict(a_count=63), -2), (dict(a_rows=0x7000, a_count=0), -2), (dict(N=0), -2), (dict(K=48), -2),
+    (dict(rows=0), -2), (dict(rows=(1 << 30) + 1, a_rows=0x7000, a_count=1), -2), (dict(a_count=63), -2), (dict(a_rows=0x7000, a_count=0), -2), (dict(N=0), -2), (dict(K=48), -2),
     (dict(K=16), -2), (dict(K=(1 << 24) + 32), -2), (dict(groups=0), -2), (dict(groups=65536), -2), (dict(ldd=255), -2),
     (dict(lda=480), -2), (dict(ldsa=15), -2), (dict(ldb=480), -2), (dict(ldsb=15), -2), (dict(strideb=-32), -2),
     (dict(strideb_scale=-1), -2), (dict(ldb=1 << 24), -2), (dict(ldsb=1 << 23), -2), (dict(lda=1 << 24), -2),
@@ -137,7 +137,7 @@ def _norm(**kw):
     (dict(T=1 << 26), -2), (dict(T=1 << 24, K=544), -2), (dict(T=1 << 23, K=4128), -2), (dict(T=1 << 22, K=8224), -2),
     (dict(ldy=32), -2), (dict(ldx=32), -2),
     (dict(gate=0x9000, ldg=32), -2), (dict(ldh=32), -2), (dict(ldz=32), -2), (dict(lda=32), -2), (dict(ldsa=1), -2),
-    (dict(top_k=2, pos=0x9000, weights=0xA000, y_rows=0), -2),
+    (dict(top_k=2, pos=0x9000, weights=0xA000, y_rows=0), -2), (dict(top_k=1025, pos=0x9000, weights=0xA000, y_rows=9), -2),
     (dict(Y=0x1008), -3), (dict(X=0x2008), -3), (dict(gate=0x9008), -3), (dict(H=0x3002), -3), (dict(Z=0x4008), -3),
     (dict(A=0x5008), -3), (dict(w_post=0x7008), -3), (dict(w_pre=0x8008), -3), (dict(ldy=68), -3), (dict(ldx=68), -3),
     (dict(gate=0x9000, ldg=68), -3), (dict(ldh=68), -3), (dict(ldz=68), -3), (dict(lda=80), -3),
