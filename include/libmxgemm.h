@@ -486,10 +486,10 @@ typedef struct mxgemm_grouped {
  * hold, no address outside the buffers is formed (they are clamped to [0,
  * rows]), and a row index outside [0, a_count) reads as a row of zeros.
  *
- * Shapes: rows, a_count, N >= 1; rows <= 2^30; 1 <= groups <= 65535; K >= 32, K % 32 == 0,
- * K <= 2^24; 256 rows of A, of B and of a scale matrix, and with a row list all
- * of A and of scaleA, below 2^31 bytes; fewer than 2^23 tiles, the smallest of
- * 32 x 128 elements of D (else MXGEMM_ERR_SHAPE).  Alignment: A, B
+ * Shapes: rows, a_count, N >= 1; rows <= 2^30; 1 <= groups <= 65535; K >= 32,
+ * K % 32 == 0, K <= 2^24; 256 rows of A, of B and of a scale matrix, and with a
+ * row list all of A and of scaleA, below 2^31 bytes; fewer than 2^23 tiles, the
+ * smallest of 32 x 128 elements of D (else MXGEMM_ERR_SHAPE).  Alignment: A, B
  * 16-byte aligned, the byte pitches of A, B and strideb multiples of 16; D 2
  * bytes, offsets and a_rows 4 bytes.  D must not overlap an input.
  * Asynchronous on `stream`; errors as mxgemm_run.
