@@ -90,7 +90,14 @@ struct GroupedTileKernel {
     GroupedLaunchFn persist[2];  // persistent (may be null): 16-byte rows of D, N % 8 == 0, K >= 256, at most kGroupTable experts
 };
 const GroupedTileKernel *grouped_tile_kernels(int *count);
-// Few rows per expert (mx_grouped.hip)
+// Few rows per expert (mx_grouped.hip): groups of up to kStreamRows rows, and
+// the most that M rows of E experts make
+constexpr int kStreamRows = 16;
+constexpr int grouped_stream_lines(int M, int E)
+{
+    const int some = E < M ? E : M;  // experts that can have rows
+    return some + (M - some) / kStreamRows;
+}
 void launch_grouped_stream(bool fp8, const GroupedArgs &g, hipStream_t s);
 
 }  // namespace mx

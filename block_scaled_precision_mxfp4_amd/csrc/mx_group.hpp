@@ -15,25 +15,29 @@ __device__ __forceinline__ void group_range(const int32_t *offsets, int E, int r
     hi = e < E ? min(max(offsets[e + 1], 0), rows) : 0;
 }
 
-// The nth expert that has rows (from 0): its number and row range; false if
-// there are fewer.
-__device__ __forceinline__ bool nth_group(const int32_t *offsets, int E, int rows, int nth, int lane, int &e, int &m0,
-                                          int &m1)
+// The nth group (from 0) of up to bm rows of one expert, counted through the
+// experts in order: the expert, the group's first row and the expert's end;
+// false if there are fewer.
+__device__ __forceinline__ bool nth_rows(const int32_t *offsets, int E, int rows, int bm, int nth, int lane, int &e, int &m0,
+                                         int &m1)
 {
     for (int e0 = 0; e0 < E; e0 += 64) {
         int lo, hi;
         group_range(offsets, E, rows, e0 + lane, lo, hi);
-        const uint64_t some = __ballot(hi > lo);
-        const int n = __popcll(some);
-        if (nth < n) {
-            const bool it = hi > lo && __popcll(some & ((1ull << lane) - 1)) == nth;
-            const int at = __ffsll((unsigned long long)__ballot(it)) - 1;
+        const int n = (max(hi - lo, 0) + bm - 1) / bm;
+        const int upto = wave_scan(n);
+        const uint64_t past = __ballot(nth < upto);
+        if (past) {
+            const int at = __ffsll((unsigned long long)past) - 1;
+            const int first = __builtin_amdgcn_readlane(lo, at);
             e = e0 + at;
-            m0 = __builtin_amdgcn_readlane(lo, at);
+            m0 = first + (nth - __builtin_amdgcn_readlane(upto - n, at)) * bm;
             m1 = __builtin_amdgcn_readlane(hi, at);
-            return true;
+            // (offsets that do not ascend can make the sums overflow:
+            // whatever came out, the rows are the expert's)
+            return m0 >= first && m0 < m1;
         }
-        nth -= n;
+        nth -= __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }

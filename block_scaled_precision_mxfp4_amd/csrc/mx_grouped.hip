@@ -3,13 +3,16 @@
 // Expert e's rows offsets[e] .. offsets[e+1]-1 of D are its rows of A times
 // its B[e]^T.  With few rows the call is bound by the time to the first bytes
 // and then by reading the B of every expert that has rows, once.  The grid has
-// a line of workgroups for each of at most min(E, rows) such experts (found
-// from the offsets by one ballot per 64 experts).  A workgroup's four waves
+// a line of workgroups for each group of up to 16 rows of one expert, as many as
+// the rows can make (found from the offsets by a scan of each 64 experts): an
+// expert with many rows has as many lines, which share its B in L2, and not one
+// that passes over B again and again (64 experts, N = 256, K = 2048, 1024 rows
+// of which one expert has all: X us against 189 with passes, FP8 X
+// against 247).  A workgroup's four waves
 // take 64 / KS rows of B, KS waves sharing 16 rows and splitting K in pieces
 // of 512 that go straight into registers, DEPTH pieces in flight per wave; the
 // waves of a row group add their sums through LDS in a fixed order.  The first
 // pieces of B are asked for before the row list, whose answer only A needs.
-// An expert with more than 16 rows is done in several passes over B.
 #include "mx_device.hpp"
 #include "mx_experts.hpp"
 #include "mx_group.hpp"
@@ -27,8 +30,8 @@ __global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ks = wave % KS, wr = wave / KS;  // K share, row group
-    int e, m0, m1;
-    if (!nth_group(g.offsets, g.E, g.M, blockIdx.y, lane, e, m0, m1))
+    int e, m, m1;  // expert, its first row here, its end
+    if (!nth_rows(g.offsets, g.E, g.M, kStreamRows, blockIdx.y, lane, e, m, m1))
         return;
     const int n0 = (blockIdx.x * (4 / KS) + wr) * 16;
     const int rows_b = max(0, min(16, g.N - n0));  // (a row group past N reads and writes nothing)
@@ -54,78 +57,75 @@ __global__ void __launch_bounds__(256) mx_grouped_stream_kernel(GroupedArgs g)
         }
     };
 
-    for (int m = m0; m < m1; m += 16) {
-        Piece p[DEPTH];
+    Piece p[DEPTH];
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            load_b(ks + d * KS, p[d]);
-        // this pass's row of A: through the row list, or from row m on
-        const int64_t first = g.a_rows ? 0 : m;
-        const int a_rows = g.a_rows ? g.a_count : min(16, m1 - m);
-        int row = m + q < m1 ? (g.a_rows ? g.a_rows[m + q] : q) : -1;
-        const bool on = (uint32_t)row < (uint32_t)a_rows;
-        row = on ? row : 0;
-        const auto ra = make_rsrc_u(g.A + first * g.lda_b, (uint32_t)((a_rows - 1) * g.lda_b + (int64_t)g.KB * AKB));
-        const auto rsa = make_rsrc_u(g.SA + first * g.ldsa, (uint32_t)((a_rows - 1) * g.ldsa + g.KB));
-        const uint32_t a_lane = (uint32_t)(row * g.lda_b + j * 16);
-        auto load_a = [&](int u, Piece &p) __attribute__((always_inline)) {
-            p.sa = load_scale_raw<SVEC>(rsa, g.ldsa, row, u * 16, on ? g.KB : 0, lane);
+    for (int d = 0; d < DEPTH; ++d)
+        load_b(ks + d * KS, p[d]);
+    // the lane's row of A: through the row list, or from row m on
+    const int64_t first = g.a_rows ? 0 : m;
+    const int a_rows = g.a_rows ? g.a_count : min(16, m1 - m);
+    int row = m + q < m1 ? (g.a_rows ? g.a_rows[m + q] : q) : -1;
+    const bool on = (uint32_t)row < (uint32_t)a_rows;
+    row = on ? row : 0;
+    const auto ra = make_rsrc_u(g.A + first * g.lda_b, (uint32_t)((a_rows - 1) * g.lda_b + (int64_t)g.KB * AKB));
+    const auto rsa = make_rsrc_u(g.SA + first * g.ldsa, (uint32_t)((a_rows - 1) * g.ldsa + g.KB));
+    const uint32_t a_lane = (uint32_t)(row * g.lda_b + j * 16);
+    auto load_a = [&](int u, Piece &p) __attribute__((always_inline)) {
+        p.sa = load_scale_raw<SVEC>(rsa, g.ldsa, row, u * 16, on ? g.KB : 0, lane);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int kb = u * 16 + s * 4;
-                const uint32_t o = a_lane + (uint32_t)(kb * AKB);
-                if constexpr (FP8) {
-                    // K 16j.. and 64 + 16j.. of the step
-                    const v4i lo = load16(ra, on && kb + j / 2 < g.KB ? o : kOOB);
-                    const v4i hi = load16(ra, on && kb + 2 + j / 2 < g.KB ? o + 64 : kOOB);
-                    p.a[s] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                } else {
-                    p.a[s] = load16(ra, on && kb + j < g.KB ? o : kOOB);
-                }
-            }
-        };
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            load_a(ks + d * KS, p[d]);
-        v4f acc = {0.f, 0.f, 0.f, 0.f};
-        auto multiply = [&](const Piece &p) __attribute__((always_inline)) {
-            const int sbw = (int)scale_group_word<SVEC>(p.sb, lane), saw = (int)scale_group_word<SVEC>(p.sa, lane);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if constexpr (FP8)
-                    acc = mma_sel_wide<kFmtHw[1]>(s, s, p.b[s], p.a[s], acc, sbw, saw);
-                else
-                    acc = mma_sel(s, s, p.b[s], p.a[s], acc, sbw, saw);
-            }
-        };
-        int u = ks;
-        for (; u + KS * DEPTH < units; u += KS * DEPTH) {
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                multiply(p[d]);
-                load_b(u + (DEPTH + d) * KS, p[d]);
-                load_a(u + (DEPTH + d) * KS, p[d]);
+        for (int s = 0; s < 4; ++s) {
+            const int kb = u * 16 + s * 4;
+            const uint32_t o = a_lane + (uint32_t)(kb * AKB);
+            if constexpr (FP8) {
+                // K 16j.. and 64 + 16j.. of the step
+                const v4i lo = load16(ra, on && kb + j / 2 < g.KB ? o : kOOB);
+                const v4i hi = load16(ra, on && kb + 2 + j / 2 < g.KB ? o + 64 : kOOB);
+                p.a[s] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            } else {
+                p.a[s] = load16(ra, on && kb + j < g.KB ? o : kOOB);
             }
         }
+    };
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            multiply(p[d]);  // (zeros past K)
-        s_part[wave][lane] = acc;
-        __syncthreads();
-        if (ks == 0) {
+    for (int d = 0; d < DEPTH; ++d)
+        load_a(ks + d * KS, p[d]);
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Piece &p) __attribute__((always_inline)) {
+        const int sbw = (int)scale_group_word<SVEC>(p.sb, lane), saw = (int)scale_group_word<SVEC>(p.sa, lane);
 #pragma unroll
-            for (int w = 1; w < KS; ++w)
-                acc += s_part[wave + w][lane];
+        for (int s = 0; s < 4; ++s) {
+            if constexpr (FP8)
+                acc = mma_sel_wide<kFmtHw[1]>(s, s, p.b[s], p.a[s], acc, sbw, saw);
+            else
+                acc = mma_sel(s, s, p.b[s], p.a[s], acc, sbw, saw);
         }
-        // (the matrix instructions read every lane's operands whatever lanes
-        // are active: the sums are pinned here, or they and their operands
-        // would be moved behind the store's bounds check, where lanes outside
-        // D no longer make theirs)
-        asm volatile("" : "+v"(acc));
-        if (ks == 0)
-            store_quad(ep, m + q, n0 + 4 * j, acc);
-        __syncthreads();
+    };
+    int u = ks;
+    for (; u + KS * DEPTH < units; u += KS * DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            multiply(p[d]);
+            load_b(u + (DEPTH + d) * KS, p[d]);
+            load_a(u + (DEPTH + d) * KS, p[d]);
+        }
     }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        multiply(p[d]);  // (zeros past K)
+    s_part[wave][lane] = acc;
+    __syncthreads();
+    if (ks == 0) {
+#pragma unroll
+        for (int w = 1; w < KS; ++w)
+            acc += s_part[wave + w][lane];
+    }
+    // (the matrix instructions read every lane's operands whatever lanes
+    // are active: the sums are pinned here, or they and their operands
+    // would be moved behind the store's bounds check, where lanes outside
+    // D no longer make theirs)
+    asm volatile("" : "+v"(acc));
+    if (ks == 0)
+        store_quad(ep, m + q, n0 + 4 * j, acc);
 }
 
 // Two waves a row group, two pieces in flight each.  On MI355X (32 experts, N =
@@ -139,7 +139,7 @@ template <bool FP8>
 static void launch_stream_as(const GroupedArgs &g, hipStream_t s)
 {
     constexpr int R = 64 / kStreamKs;  // rows of B per workgroup
-    const dim3 grid((unsigned)((g.N + R - 1) / R), (unsigned)(g.E < g.M ? g.E : g.M));
+    const dim3 grid((unsigned)((g.N + R - 1) / R), (unsigned)grouped_stream_lines(g.M, g.E));
     if (g.scale16)
         hipLaunchKernelGGL((mx_grouped_stream_kernel<FP8, true, kStreamKs, kStreamDepth>), grid, dim3(256), 0, s, g);
     else

@@ -288,7 +288,7 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
         return st;
     const int kernel = plan_grouped(rows, N, groups, bits, cu);
     if (kernel < 0) {
-        if (cdiv(N, 32) * 256 >= kMaxThreads)
+        if (cdiv(N, 32) * 256 >= kMaxThreads || mx::grouped_stream_lines(rows, groups) > 65535)
             return MXGEMM_ERR_SHAPE;
         mx::launch_grouped_stream(bits == 8, g, stream);
         return launched();

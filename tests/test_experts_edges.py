@@ -1,0 +1,61 @@
+"""GPU tests of the mixture-of-experts operators at their edges: routings that
+give one expert everything, weights of masked tokens against a bound that does
+not grow with the mask, and the persistent product on bad rows and offsets."""
+import numpy as np
+import pytest
+
+import block_scaled_precision_mxfp4_amd as mx
+import experts_ref as ref
+from block_scaled_precision_mxfp4_amd import inputs
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+from mxgpu import dev_u8, host_bits  # noqa: E402
+from test_experts import dev, run_grouped, say  # noqa: E402
+
+
+# ---- product grouped by expert: streaming ---------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+@pytest.mark.parametrize("kind", ["one", "even", "ragged"])
+@pytest.mark.parametrize("rows,E,N,K", [(1024, 64, 256, 512), (1000, 70, 40, 544), (33, 3, 100, 1056), (520, 130, 24, 96)])
+def test_grouped_streamed_groups_of_rows(rows, E, N, K, kind, fp8, monkeypatch):
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", "-1")
+    run_grouped(np.random.default_rng(rows + K), rows, E, N, K, fp8, kind, gather=rows // 3, what="streamed")
+    run_grouped(np.random.default_rng(rows + K), rows, E, N, K, fp8, kind, what="streamed")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp4", "fp8"])
+def test_grouped_one_expert_with_all_rows_is_not_serial(fp8, monkeypatch):
+    """Rows that the plan streams because their experts' tiles would be few (64 experts, N = 256), all of one expert's: done
+    one group of 16 after another they took 24 times the time of the smallest tile, side by side they take about as long."""
+    rows, E, N, K = 1024, 64, 256, 2048
+    w = 1 if fp8 else 2
+    A, SA = torch.randint(0, 120, (rows, K // w), dtype=torch.uint8, device="cuda"), torch.full((rows, K // 32), 120, dtype=torch.uint8, device="cuda")
+    B, SB = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda"), torch.full((E, N, K // 32), 120, dtype=torch.uint8, device="cuda")
+    off = dev(np.where(np.arange(E + 1) <= E // 2, 0, rows).astype(np.int32))
+    D = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+
+    def us(tile):
+        if tile is None:
+            monkeypatch.delenv("MXGEMM_GROUPED_TILE", raising=False)
+        else:
+            monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+        call = lambda: mx.mxgemm_grouped_run(D, A, B, SA, SB, off, rows, N, K, E, a_format=1 if fp8 else 0)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        best = []
+        for _ in range(9):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(8):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b) * 125)
+        return min(best)
+    say("case grouped one expert", fp8)
+    plan, tile = us(None), us(4)
+    say("us: plan %.1f, smallest tile %.1f" % (plan, tile))
+    assert plan < 5 * tile
