@@ -48,11 +48,16 @@ int route_blocks(int T, int unit) { return (int)cdiv(cdiv(T, unit), route_units_
 
 // The grouped product's kernel: an index into the tiles, or -1 for streaming.
 // The host knows the rows and experts, not how the rows are spread.
-//   - A handful of rows whose experts' tiles (128 columns each) would leave
-//     compute units idle are streamed: one token of the table's shape 7.2
-//     against 8.0 us on the 32-row tile (FP4), 7.3 against 12.8 us with 2 rows,
-//     N = 2880, K = 4096; from 8 rows on (256 tiles) the tile is as fast, and
-//     15.7 against 17.6 us for 32 rows.
+//   - Rows that make few tiles (16 an expert, and 128 columns of every expert
+//     that can have rows on less than all compute units) are streamed.  Cold
+//     weights, us, streaming / the 32-row tile, FP4 and FP8: 4 rows of 32 experts,
+//     N = 4096, K = 2048, 8.1 / 9.3 and 8.6 / 9.7; 64 of 16, N = 1024, K = 4096,
+//     12.7 / 18.6 and 13.7 / 19.4; 1024 of 64, N = 256, K = 2048, 8.8 / 10.6 and
+//     10.5 / 11.2, all of one expert's 8.0 / 7.7 and 9.7 / 8.3.  It loses on short
+//     K (K = 512 there 5.5 / 4.6 and 6.3 / 4.8) and, the most, where one of few
+//     experts has all of many rows (128 of 8, N = 2880, K = 4096, 20.3 / 12.8 and
+//     25.3 / 13.9; evenly spread 20.2 / 20.5 and 25.1 / 20.9): the host does not
+//     know how they are spread.
 //   - Else the first tile whose rows per expert are reached and whose tiles,
 //     every expert's last one half filled, occupy 3/4 of the compute units
 //     (8 experts of 128 rows, N = 2048, K = 4096, FP8: 21.1 us on 91 % of them
