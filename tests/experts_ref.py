@@ -81,6 +81,22 @@ def route_weight_tol(x, E):
     return (2 * span + 4 + E + 1) * 2.0 ** -24, 2.0 ** -126
 
 
+def route_weight_bound(x, ids):
+    """Absolute bounds [T, k] of the weights of ids (route's): relative to a weight, its own logit's distance d to its
+    token's maximum rounds once (2^-24 of itself, which the exponential turns into a relative error) and the exponential is
+    good to 2^-23; in the sum every share carries the same, of which the first is at most 1/e (d e^-d), each of up to E
+    additions and the division round to 2^-24.  A share of d > 104 is below half of fp32's least value: with it the bound
+    is fp32's smallest normal value, below which a share may be flushed or lose bits.  A logit that is masked or has the
+    type's lowest value does not widen the others' bounds."""
+    E = x.shape[1]
+    can = np.where(x > -np.inf, x, -np.inf)
+    m = can.max(1, keepdims=True)
+    with np.errstate(invalid="ignore", over="ignore"):
+        d = np.where(can == m, 0.0, np.minimum(m - can, 104.0))
+    d = np.take_along_axis(d, np.where(ids < 0, 0, ids), 1)
+    return (d + 2 + E / np.e + 2 + E + 1) * 2.0 ** -24, 2.0 ** -126
+
+
 def glu(bits, K):
     """bf16 bits [M, 2K] -> bf16 bits of silu(gate) * up [M, K]."""
     g, u = bf16_to_f64(bits[:, :K]), bf16_to_f64(bits[:, K:])

@@ -11,8 +11,42 @@ from block_scaled_precision_mxfp4_amd import inputs
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
-from mxgpu import dev_u8, host_bits  # noqa: E402
-from test_experts import dev, run_grouped, say  # noqa: E402
+from mxgpu import dev_u8  # noqa: E402
+from test_experts import dev, run_grouped, run_route, say  # noqa: E402
+from test_experts_host import special_logits  # noqa: E402
+
+
+# ---- router choice ------------------------------------------------------------
+
+def check_weights(x, k, renorm):
+    got = run_route(x, k, renorm, False)
+    x = x.astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        ids, weights, pos, offsets, rows = ref.route(x, k, renorm)
+    for name, want in (("ids", ids), ("pos", pos), ("offsets", offsets), ("rows", rows)):
+        assert np.array_equal(got[name], want), name
+    rel, small = ref.route_weight_bound(x, ids)
+    off = np.abs(got["weights"] - weights) > rel * weights + small
+    assert not off.any(), "%d weights outside, e.g. %r, not %r" % (off.sum(), got["weights"][off][0], weights[off][0])
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(50, 12, 4), (64, 200, 16), (400, 40, 5), (90, 300, 12), (70, 1024, 16), (5000, 24, 3)])
+def test_route_weights_beside_masks(T, E, k, renorm):
+    say("case route weights", T, E, k, renorm)
+    check_weights(special_logits(np.random.default_rng(T), T, E), k, renorm)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(33, 64, 6), (700, 128, 8), (66, 512, 4)])
+def test_route_weights_of_wide_logits(T, E, k, renorm):
+    """Shares from 1 down to fp32's least value, with masked logits among them."""
+    rng = np.random.default_rng(E)
+    x = (25 * rng.standard_normal((T, E))).astype(np.float32)
+    x[rng.random((T, E)) < 0.3] = -np.inf
+    x[rng.random((T, E)) < 0.1] = np.finfo(np.float32).min
+    say("case route wide", T, E, k, renorm)
+    check_weights(x, k, renorm)
 
 
 # ---- product grouped by expert: streaming ---------------------------------------

@@ -177,3 +177,31 @@ def test_fp8_codes_decode_to_their_values():
     code, scale = ref.quantize_fp8(bits)
     got = np.array([oracle.decode(1, int(c)) for c in code[0]]) * np.exp2(scale[0].astype(float) - 127).repeat(32)
     assert np.abs(got - ref.bf16_to_f64(bits)[0]).max() <= 2.0 ** -4 * 300
+
+
+def special_logits(rng, T, E):
+    """Ties, zeros of both signs, masks, NaN, infinities and the type's lowest value; tokens of which nothing is left."""
+    x = rng.integers(-2, 3, (T, E)).astype(np.float32) / 2
+    x = np.where(rng.random((T, E)) < 0.5, x, 4 * rng.standard_normal((T, E)).astype(np.float32))
+    x[rng.random((T, E)) < 0.1] = -0.0
+    x[rng.random((T, E)) < 0.4] = -np.inf
+    x[rng.random((T, E)) < 0.05] = np.nan
+    x[rng.random((T, E)) < 0.3 / E] = np.inf
+    x[rng.random((T, E)) < 0.02] = np.finfo(np.float32).min
+    x[rng.random(T) < 0.1] = -np.inf
+    x[0], x[1] = np.nan, np.finfo(np.float32).min
+    x[2], x[2, E // 2] = -np.inf, 1.0
+    x[3], x[3, 0], x[3, E - 1] = -100.0, 0.0, -90.0  # shares near fp32's least value
+    return x
+
+
+@pytest.mark.parametrize("T,E,k", [(50, 12, 4), (400, 40, 5), (90, 300, 12), (70, 1024, 16)])
+def test_route_weight_bound_is_tight_beside_masks(T, E, k):
+    x = special_logits(np.random.default_rng(T), T, E).astype(np.float64)
+    for renorm in (True, False):
+        with np.errstate(invalid="ignore"):
+            ids, w, _, _, _ = ref.route(x, k, renorm)
+        rel, small = ref.route_weight_bound(x, ids)
+        assert rel.max() < 1e-3
+        some = w > 2 * small
+        assert some.any() and (np.abs(1.001 * w - w) > rel * w + small)[some].all()  # a mistake of a thousandth is seen
