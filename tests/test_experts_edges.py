@@ -93,3 +93,42 @@ def test_grouped_one_expert_with_all_rows_is_not_serial(fp8, monkeypatch):
     plan, tile = us(None), us(4)
     say("us: plan %.1f, smallest tile %.1f" % (plan, tile))
     assert plan < 5 * tile
+
+
+# ---- product grouped by expert: the persistent 8-bit tile -------------------------
+
+@pytest.mark.parametrize("K,pads", [(512, (8, 64, 16, 32, 16)), (512, (0, 32, 3, 0, 7)), (800, (16, 16, 5, 32, 1)), (2048, (8, 0, 0, 64, 0))],
+                         ids=["whole-groups", "odd-scales", "odd-stages", "one-group-more"])
+@pytest.mark.parametrize("rows,E,N,gather", [(8300, 7, 1096, 700), (6000, 1000, 264, 100)])
+def test_grouped_persistent_rows_strides_and_alpha(rows, E, N, gather, K, pads, monkeypatch):
+    """More tiles than compute units on the persistent form (8-bit A, D in 16-byte rows): row indexes that are not there beside a
+    row 0 of NaN scales, padded strides, scale rows of any alignment, a factor."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", "1")
+    rng = np.random.default_rng(rows + K)
+    cols = np.unique(np.concatenate([rng.integers(0, N, 7), [0, N - 1]]))
+    run_grouped(rng, rows, E, N, K, True, gather=gather, alpha=-0.75, pads=pads, bad_rows=True, nan_first=True, cols=cols,
+                odd_scales=pads[2] % 2 == 1, what="persistent")
+
+
+@pytest.mark.parametrize("persist", ["0", "1"])
+@pytest.mark.parametrize("tile", [-1, 1, 3, 4])
+@pytest.mark.parametrize("rows,E,N,K", [(90, 6, 64, 512), (9000, 9, 1032, 544)])
+def test_grouped_8_bit_offsets_that_do_not_ascend_stay_inside(rows, E, N, K, tile, persist, monkeypatch):
+    """Whatever the offsets and the row list hold, nothing outside D's rows and columns is written, by any 8-bit kernel."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    monkeypatch.setenv("MXGEMM_TILE_PERSIST", persist)
+    rng = np.random.default_rng(rows)
+    wild = rng.integers(-2 ** 31, 2 ** 31, E + 1)
+    back = np.linspace(rows, 0, E + 1).astype(int)
+    over = np.where(np.arange(E + 1) % 2 == 0, 0, rows)
+    for off in (wild, back, over, rng.integers(0, rows + 1, E + 1)):
+        whole = torch.full((rows + 64, N + 16), 11.0, dtype=torch.bfloat16, device="cuda")
+        D = whole[32:32 + rows, 8:]
+        a_rows = np.where(rng.random(rows) < 0.2, rng.integers(-2 ** 31, 2 ** 31, rows), rng.integers(0, 50, rows)).astype(np.int32)
+        say("case grouped offsets", tile, persist, rows, off)
+        mx.mxgemm_grouped_run(D, dev_u8(inputs.wide_codes(1, 50, K, 1)), dev_u8(inputs.fp4_codes_packed(2, E * N, K)),
+                              dev_u8(inputs.e8m0_scales(3, 50, K, 120, 130)), dev_u8(inputs.e8m0_scales(4, E * N, K, 120, 130)),
+                              dev(off.astype(np.int32)), rows, N, K, E, a_rows=dev(a_rows), a_count=50, a_format=1, ldd=N + 16)
+        torch.cuda.synchronize()
+        assert (whole[:32] == 11).all() and (whole[32 + rows:] == 11).all()
+        assert (whole[:, :8] == 11).all() and (whole[:, 8 + N:] == 11).all()
