@@ -407,11 +407,9 @@ __global__ void __launch_bounds__(64 * WM * WN) mx_tile_grouped_kernel(GroupedAr
     set_tile_a();
     issue_operands(0, true, B0{}, std::integral_constant<int, PERSIST ? 3 : 1>{});
     if (!SVEC && !PERSIST && g.KB < 8) {
-        // one stage: the one that its prefetch asks for, which is not used,
-        // would read before or behind a row (there are at least two offsets)
+        // (one stage, with no scale loads of its own: the first stage's bring
+        // those of two)
         x_any[0] = load_scale_row_short(x_base, x_row, g.KB);
-        x_base = (const global_u8 *)(uintptr_t)g.offsets;
-        x_row = 0;
     } else {
         issue_scales(0, true, B0{});
     }
