@@ -72,7 +72,8 @@ class Info(ctypes.Structure):
         return d
 
 
-# (the two structs below are passed packed: a fifth of a Structure's time)
+# (the functions below pass these two packed, in a fifth of a Structure's time;
+# lib()'s entry points take either: a byref, or the bytes)
 class Grouped(ctypes.Structure):
     _fields_ = [("ldd", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64), ("ldb", ctypes.c_int64),
                 ("ldsb", ctypes.c_int64), ("strideb", ctypes.c_int64), ("strideb_scale", ctypes.c_int64),
@@ -130,11 +131,11 @@ def lib():
         L.mxgemm_route_workspace_bytes.argtypes = [i32, i32]
         L.mxgemm_route_workspace_bytes.restype = ctypes.c_size_t
         L.mxgemm_grouped_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, i32, i32, i32, i32,
-                                         ctypes.c_char_p, vp]
+                                         vp, vp]
         L.mxgemm_grouped_run.restype = i32
         L.mxgemm_glu_quantize.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i64, i32, vp]
         L.mxgemm_glu_quantize.restype = i32
-        L.mxgemm_norm_quantize.argtypes = [ctypes.c_char_p, i32, i32, vp]
+        L.mxgemm_norm_quantize.argtypes = [vp, i32, i32, vp]
         L.mxgemm_norm_quantize.restype = i32
         L.mxgemm_query.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
         L.mxgemm_query.restype = i32

@@ -52,6 +52,23 @@ def test_packed_structs_are_the_structs():
         assert pack(*v) == bytes(cls(*v))
 
 
+def test_structs_pass_to_the_library():
+    """A caller's own structs, by reference, by pointer, packed, or none."""
+    L = mx.lib()
+    g = mx.Grouped(256, 512, 16, 512, 16, 256 * 512, 256 * 16, 0)
+    n = mx.Norm(Y=0x1000, ldy=64, H=0x3000, ldh=64, eps=1e-6)
+
+    def grouped(p):
+        return L.mxgemm_grouped_run(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x6000, None, 1.0, 64, 64, 256, 512, 8, p, 0)
+    for way in (ctypes.byref, ctypes.pointer, bytes):
+        g.ldd, g.a_format, n.ldy, n.eps = 255, 0, 64, 0.0
+        assert grouped(way(g)) == -2 and L.mxgemm_norm_quantize(way(n), 4, 64, 0) == -1
+        g.ldd, g.a_format, n.ldy, n.eps = 256, 2, 32, 1e-6
+        assert grouped(way(g)) == -1 and L.mxgemm_norm_quantize(way(n), 4, 64, 0) == -2
+    assert L.mxgemm_norm_quantize(None, 4, 64, 0) == -1
+    assert L.mxgemm_grouped_run(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x6000, None, 1.0, 64, 64, 256, 48, 8, None, 0) == -2
+
+
 def _route(**kw):
     a = dict(ids=0x1000, weights=0x2000, pos=0x3000, offsets=0x4000, rows=0x5000, logits=0x6000, T=64, E=32, top_k=4,
              workspace=None, workspace_bytes=0, stream=0)
