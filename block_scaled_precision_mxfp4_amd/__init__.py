@@ -166,10 +166,11 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without building the Stream
-        # object (0.3 against 2.8 us, as much as the launch itself)
+        # torch.cuda.current_stream().cuda_stream, where torch has it without
+        # building the Stream object (0.3 against 2.8 us, as much as the launch)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

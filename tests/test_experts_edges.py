@@ -132,3 +132,14 @@ def test_grouped_8_bit_offsets_that_do_not_ascend_stay_inside(rows, E, N, K, til
         torch.cuda.synchronize()
         assert (whole[:32] == 11).all() and (whole[32 + rows:] == 11).all()
         assert (whole[:, :8] == 11).all() and (whole[:, 8 + N:] == 11).all()
+
+
+# ---- streams ----------------------------------------------------------------------
+
+def test_calls_go_to_torchs_current_stream():
+    """By default a call is on torch's current stream, also inside a stream context."""
+    s = torch.cuda.Stream()
+    assert mx._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(s):
+        assert mx._stream(None) == s.cuda_stream == mx._stream(s)
+    assert mx._stream(None) == torch.cuda.current_stream().cuda_stream

@@ -69,6 +69,13 @@ def test_structs_pass_to_the_library():
     assert L.mxgemm_grouped_run(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x6000, None, 1.0, 64, 64, 256, 48, 8, None, 0) == -2
 
 
+def test_current_stream_without_torchs_raw_getter(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), {"cuda_stream": 0x1230}))
+    assert mx._stream(None) == 0x1230 and mx._stream(7) == 7
+
+
 def _route(**kw):
     a = dict(ids=0x1000, weights=0x2000, pos=0x3000, offsets=0x4000, rows=0x5000, logits=0x6000, T=64, E=32, top_k=4,
              workspace=None, workspace_bytes=0, stream=0)
