@@ -28,12 +28,17 @@ int elem_bits(int a_format)
     return a_format == MXGEMM_FMT_FP4 ? 4 : a_format == MXGEMM_FMT_FP8_E4M3 ? 8 : 0;
 }
 
+// Bytes of a row of lda elements, and whether they are a multiple of 16: no
+// product that a stride of any size could overflow
+int64_t row_bytes(int64_t lda, int bits) { return bits == 4 ? lda / 2 : lda; }
+bool row_aligned(int64_t lda, int bits) { return lda % (128 / bits) == 0; }
+
 // A quantized output (rows of lda elements): extents, then alignment
 mxgemm_status check_quantized(const void *A, int K, int64_t lda, int64_t ldsa, int bits)
 {
     if (lda < K || ldsa < K / 32)
         return MXGEMM_ERR_SHAPE;
-    if (!aligned(A, 16) || (lda * bits) % 128)
+    if (!aligned(A, 16) || !row_aligned(lda, bits))
         return MXGEMM_ERR_ALIGN;
     return MXGEMM_OK;
 }
@@ -169,7 +174,7 @@ mxgemm_status mxgemm_glu_quantize(void *A, void *scaleA, const void *X, const in
     q.M = M;
     q.K = K;
     q.ldx = ldx;
-    q.lda_b = lda * bits / 8;
+    q.lda_b = row_bytes(lda, bits);
     q.lds = ldsa;
     q.blocks = blocks;
     q.fp8 = bits == 8;
@@ -225,7 +230,7 @@ mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream
     a.ldx = n->ldx;
     a.ldh = n->ldh;
     a.ldz = n->ldz;
-    a.lda_b = n->lda * bits / 8;
+    a.lda_b = row_bytes(n->lda, bits);
     a.lds = n->ldsa;
     a.res_scale = n->res_scale;
     a.eps = n->eps;
@@ -250,11 +255,11 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
         groups > 65535 || s.ldd < N || s.lda < K || s.ldsa < K / 32 || s.ldb < K || s.ldsb < K / 32 || s.strideb < 0 ||
         s.strideb_scale < 0)
         return MXGEMM_ERR_SHAPE;
-    if (s.lda % 2 || s.ldb % 2 || s.strideb % 2 || !aligned(A, 16) || !aligned(B, 16) || (s.lda * bits) % 128 ||
+    if (s.lda % 2 || s.ldb % 2 || s.strideb % 2 || !aligned(A, 16) || !aligned(B, 16) || !row_aligned(s.lda, bits) ||
         (s.ldb / 2) % 16 || (s.strideb / 2) % 16 || !aligned(D, 2) || !aligned(offsets, 4) || !aligned(a_rows, 4))
         return MXGEMM_ERR_ALIGN;
     mx::GroupedArgs g = {};
-    g.lda_b = s.lda * bits / 8;
+    g.lda_b = row_bytes(s.lda, bits);
     g.ldb_b = s.ldb / 2;
     // the kernels address a tile's rows of B, and through a row list all of
     // A, with 32-bit offsets

@@ -129,6 +129,15 @@ def test_grouped_refusals(kw, code):
     assert _grouped(**kw) == code
 
 
+@pytest.mark.parametrize("lda", [1 << 61, (1 << 62) - 32, 1 << 62, (1 << 62) + 32, (1 << 63) - 128])
+@pytest.mark.parametrize("a_format", [0, 1])
+@pytest.mark.parametrize("a_rows", [None, 0x7000])
+def test_grouped_strides_past_64_bits_are_refused(lda, a_format, a_rows):
+    """Strides whose bits are more than 64 bits count: their rows are past every span, not at a pitch of the low bits."""
+    assert _grouped(lda=lda, a_format=a_format, a_rows=a_rows) == -2
+    assert _grouped(ldb=lda, strideb=0, a_format=a_format, a_rows=a_rows) == -2
+
+
 def _glu(**kw):
     a = dict(A=0x1000, scaleA=0x2000, X=0x3000, M=4, K=64, stream=0)
     a.update(kw)
