@@ -2,10 +2,12 @@
 // rows [gate 0..K-1 | up K..2K-1] in bf16, and v's 32-blocks in MXFP4 or
 // MXFP8, in one pass: v itself never reaches memory.
 //
-// silu(g) u = g u / (1 + e^-g).  v is the correctly rounded bf16 value, so
+// silu(g) u = g u / (1 + e^-g).  v is that in 64 bits, rounded once to bf16, so
 // that codes and scales do not depend on how the exponential was computed: it
 // is evaluated in fp32, and again in 64 bits only where fp32's error leaves
 // the bf16 rounding open (1 element in 4000) or its range does not carry it.
+// (64 bits round as the exact value does, but where they leave 1 + e^-g at 1 or
+// 2, g > 36 or |g| < 2^-50, and g u or g u / 2 is a tie between bf16 values.)
 //
 // Bound by HBM: 4 bytes read and 17/32 (FP4) or 33/32 (FP8) byte written per
 // element, each once.  Four lanes share a block and hold 8 elements each.

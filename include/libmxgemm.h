@@ -505,10 +505,14 @@ mxgemm_status mxgemm_grouped_run(void *D, const void *A, const void *B, const vo
  *
  *     v = bf16( gate / (1 + e^-gate) * up ),    (A, scaleA) = quantized v,
  *
- * v correctly rounded to nearest even, so that the result is exact in
- * mxgemm_quantize's sense (deterministic, independent of launch shape).  A
- * gate or up that is infinite or NaN makes v what IEEE arithmetic makes it
- * (-inf / inf: NaN); its block then has scale 0xFF and codes 0.
+ * v rounded once from 64 bits, to nearest even, so that the result does not
+ * depend on the launch's shape or on how the exponential was computed.  That
+ * is the exact value's rounding but for one case: where 64 bits leave 1 +
+ * e^-gate at 1 or 2 (gates above 36, or nearer to 0 than 2^-50) and gate * up, or
+ * half of it, lies in the middle between two bf16 values, the tie may decide
+ * instead of what the exact value is beside it.  A gate or up that is infinite
+ * or NaN makes v what IEEE arithmetic makes it (-inf / inf: NaN); its block then
+ * has scale 0xFF and codes 0.
  *
  * live: NULL, or a device int32 (offsets + groups, say): only rows below *live
  * (clamped to [0, M]) are read and written.  Shapes: M >= 1, K >= 32, K % 32

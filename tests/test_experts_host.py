@@ -2,10 +2,13 @@
 refusal comes before any HIP call, struct layouts match the header, and the
 64-bit implementations the GPU tests compare with are checked themselves."""
 import ctypes
+import decimal
+import math
 import os
 import shutil
 import subprocess
 import tempfile
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -238,3 +241,31 @@ def test_route_weight_bound_is_tight_beside_masks(T, E, k):
         assert rel.max() < 1e-3
         some = w > 2 * small
         assert some.any() and (np.abs(1.001 * w - w) > rel * w + small)[some].all()  # a mistake of a thousandth is seen
+
+
+def test_glu_is_the_exact_rounding_but_for_ties_at_its_ends():
+    """ref.glu (64 bits, rounded once) against 60 digits: the same bf16 value, unless gate * up or half of it is exactly in
+    the middle between two bf16 values at a gate above 36 or below 2^-50 in magnitude; there the tie may go to even."""
+    def rounded(v):  # to bf16, exactly; and whether v is a tie
+        step = Fraction(2) ** max(math.frexp(float(v))[1] - 8, -133)
+        return round(v / step) * step, (2 * v / step) % 2 == 1
+    rng = np.random.default_rng(5)
+    g = np.concatenate([rng.uniform(30, 45, 1500), 2.0 ** rng.uniform(5.2, 7, 300), rng.uniform(-60, 30, 700),
+                        rng.choice([-1, 1], 1500) * 2.0 ** rng.uniform(-60, -40, 1500)])
+    bits = np.stack([ref.f64_to_bf16(g), ref.f64_to_bf16(rng.standard_normal(len(g)))])
+    got = ref.bf16_to_f64(ref.glu(bits.T.copy(), 1)[:, 0])
+    g, u = ref.bf16_to_f64(bits)
+    ties = off = 0
+    with decimal.localcontext() as c:
+        c.prec = 60
+        for i in range(len(g)):
+            v = decimal.Decimal(g[i]) / (1 + (-decimal.Decimal(g[i])).exp()) * decimal.Decimal(u[i])
+            exact, _ = rounded(Fraction(v))
+            even, tie = rounded(Fraction(g[i]) * Fraction(u[i]) / (1 if g[i] > 1 else 2))
+            if tie and (g[i] > 36 or abs(g[i]) < 2.0 ** -50):
+                ties += 1
+                off += Fraction(got[i]) != exact
+                assert Fraction(got[i]) in (even, exact), (g[i], u[i], got[i])
+            else:
+                assert Fraction(got[i]) == exact, (g[i], u[i], got[i])
+    assert ties > 20 and off > 5  # the exception is there
