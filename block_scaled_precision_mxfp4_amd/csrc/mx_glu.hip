@@ -81,8 +81,7 @@ __global__ void __launch_bounds__(256) mx_glu_kernel(GluArgs q)
     const int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
     const int kbn = q.K >> 5;
     const int64_t live_rows = q.live ? min((int64_t)max(*q.live, 0), (int64_t)q.M) : q.M;
-    // (64-bit division is a long sequence: only where the count needs it)
-    const int64_t row = q.blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)b / (uint32_t)kbn) : b / kbn;
+    const int64_t row = (uint32_t)b / (uint32_t)kbn;  // (blocks: below 2^30)
     const int elem = (int)(b - row * kbn) * 32 + j * 8;
     const bool on = row < live_rows;
     v4i xg = {0, 0, 0, 0}, xu = xg;
