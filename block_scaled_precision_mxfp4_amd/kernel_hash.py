@@ -18,6 +18,8 @@ FAMILY_FILES = {
     "rows": _COMMON + ("mx_skinny_rows.hip",),
     "quant": _COMMON + ("mx_quant.hip", "mx_quantize.hpp"),
     "stream": _COMMON + ("mx_stream.hip",),
+    "experts": _COMMON + ("mx_experts.hpp", "mx_route.hip", "mx_group.hpp", "mx_grouped.hip", "mx_tile_grouped.hip", "mx_glu.hip",
+                          "mx_norm.hip", "mx_quantize.hpp", "mx_quantize_out.hpp", "mx_rows16.hpp"),
 }
 
 

@@ -269,3 +269,16 @@ def test_glu_is_the_exact_rounding_but_for_ties_at_its_ends():
             else:
                 assert Fraction(got[i]) == exact, (g[i], u[i], got[i])
     assert ties > 20 and off > 5  # the exception is there
+
+
+def test_fingerprint_covers_what_the_kernels_are_built_from():
+    import re
+    from block_scaled_precision_mxfp4_amd import kernel_hash as kh
+    csrc = os.path.join(ROOT, "block_scaled_precision_mxfp4_amd", "csrc")
+    need, todo = set(), ["mx_route.hip", "mx_grouped.hip", "mx_tile_grouped.hip", "mx_glu.hip", "mx_norm.hip"]
+    while todo:
+        f = todo.pop()
+        if f not in need:
+            need.add(f)
+            todo += re.findall(r'#include "(mx_[a-z0-9_]+\.hpp)"', open(os.path.join(csrc, f)).read())
+    assert need <= set(kh.FAMILY_FILES["experts"]) and len(kh.kernel_family_hash("experts")) == 16
