@@ -539,15 +539,20 @@ static void launch_tile_grouped(const GroupedArgs &g, int64_t grid, hipStream_t 
         hipLaunchKernelGGL((mx_tile_grouped_kernel<BM, BN, WM, WN, false, FP8, PERSIST>), wgs, threads, 0, s, g);
 }
 
-// The tiles, largest first, with the mean rows per expert from which each was
-// the fastest (MI355X, 32 experts, N = 4096, K = 2048, routings as uneven as a
-// softmax of normal logits; us, FP4 / FP8 A):
+// The tiles, largest first, with the mean rows per expert from which each is
+// taken (MI355X, 32 experts, N = 4096, K = 2048, routings as uneven as a softmax
+// of normal logits, weights that the last-level cache does not hold; us, FP4 /
+// FP8 A):
 //   rows per expert   4            16           64           256          1024
-//   32 x 128          - / 17.1     31.2 / 32.8  52.1 / 54.5  130 / 138    413 / -
-//   64 x 128          - / 21.0     31.3 / 31.0  42.6 / 50.5  92.6 / 121   288 / -
-//   128 x 128         - / 32.0     32.3 / 48.8  43.8 / 65.6  83.5 / 139   245 / -
-//   128 x 256         - / 27.1     - / 37.2     - / 50.8     - / 97.8     - / 289
-//   256 x 256         -            43.3 / -     57.0 / -     88.3 / -     207 / -
+//   32 x 128          28.3 / 30.2  35.8 / 37.3  52.3 / 55.3  132 / 141    404 / 445
+//   64 x 128          29.1 / 32.0  37.5 / 36.4  45.3 / 53.2  92.3 / 119   283 / 390
+//   128 x 128         31.8 / -     35.9 / -     47.3 / -     79.7 / -     247 / -
+//   128 x 256         - / 37.5     - / 39.8     - / 56.0     - / 91.6     - / 288
+//   256 x 256         38.4 / -     43.4 / -     54.0 / -     74.9 / -     195 / -
+//   bytes / 5.1 TB/s  28           29           32           43 / 45      88 / 94
+// The one taken is a column's fastest but for FP4 at 16 and 256 rows, 5 and 6 %
+// slower here; with fewer experts or columns the larger tiles leave compute units
+// idle.
 const GroupedTileKernel *grouped_tile_kernels(int *count)
 {
     static const GroupedTileKernel table[] = {
