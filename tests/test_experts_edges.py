@@ -143,3 +143,34 @@ def test_calls_go_to_torchs_current_stream():
     with torch.cuda.stream(s):
         assert mx._stream(None) == s.cuda_stream == mx._stream(s)
     assert mx._stream(None) == torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("persist", ["0", "1"])
+@pytest.mark.parametrize("K", [96, 288, 544, 800])
+@pytest.mark.parametrize("tile", [-1, 1, 3, 4])
+def test_grouped_8_bit_nan_codes_behind_k_are_not_seen(tile, K, persist, monkeypatch):
+    """Rows of A padded with NaN codes behind K, in sizes that end inside a step, a stage and a pair of stages; with more tiles
+    than compute units too."""
+    monkeypatch.setenv("MXGEMM_GROUPED_TILE", str(tile))
+    monkeypatch.setenv("MXGEMM_TILE_PERSIST", persist)
+    rng = np.random.default_rng(K)
+    N, E, pad = 264, 3, 160
+    for rows in (70, 17000):
+        A = torch.full((rows, K + pad), 0x7F, dtype=torch.uint8, device="cuda")
+        A[1::2, K:] = 0xFF
+        A[:, :K] = 0x38  # 1
+        B = torch.full((E, N, (K + pad) // 2), 0x77, dtype=torch.uint8, device="cuda")
+        B[:, :, :K // 2] = 0x22  # 1, 1
+        KB = K // 32
+        S = torch.full((rows, KB + 5), 0xFF, dtype=torch.uint8, device="cuda")
+        S[:, :KB] = 127
+        SB = torch.full((E, N, KB + 5), 0xFF, dtype=torch.uint8, device="cuda")
+        SB[:, :, :KB] = 127
+        off = np.array([0, rows // 3, rows // 3, rows], np.int32)
+        a_rows = dev(rng.integers(0, rows, rows).astype(np.int32))
+        D = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+        say("case grouped NaN behind K", tile, K, persist, rows)
+        mx.mxgemm_grouped_run(D, A, B, S, SB, dev(off), rows, N, K, E, a_rows=a_rows, a_count=rows, a_format=1, lda=K + pad,
+                              ldb=K + pad, ldsa=KB + 5, ldsb=KB + 5)
+        torch.cuda.synchronize()
+        assert (D == K).all()
