@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(_HERE, "libmxgemm.so")
 EXPORTS = ("mxgemm_status_string", "mxgemm_run", "mxgemm_run_noalloc", "mxgemm_run_bf16a", "mxgemm_pack_b", "mxgemm_pack_scales", "mxgemm_pack_a",
            "mxgemm_pack_a_bytes", "mxgemm_quantize",
            "mxgemm_f16_run", "mxgemm_route", "mxgemm_route_workspace_bytes", "mxgemm_grouped_run", "mxgemm_glu_quantize",
-           "mxgemm_norm_quantize", "mxgemm_query", "mxgemm_plan", "mxgemm_query_ex", "mxgemm_plan_ex",
+           "mxgemm_norm_quantize", "mxgemm_kv_append", "mxgemm_rope_frequencies", "mxgemm_paged_attention",
+           "mxgemm_paged_attention_workspace_bytes", "mxgemm_query", "mxgemm_plan", "mxgemm_query_ex", "mxgemm_plan_ex",
            "mxgemm_stream_read", "mxgemm_release_workspaces")
 
 STATUS = {0: "MXGEMM_OK", -1: "MXGEMM_ERR_INVALID_ARG", -2: "MXGEMM_ERR_SHAPE",
@@ -52,6 +53,7 @@ SPLIT_BF16_ATOMIC = 1  # MXGEMM_SPLIT_BF16_ATOMIC
 FMT_FP4, FMT_FP8_E4M3, FMT_FP8_E5M2, FMT_FP6_E2M3, FMT_FP6_E3M2 = 0, 1, 2, 3, 4
 FORMAT_BITS = (4, 8, 8, 6, 6)
 B_NK, B_KN = 0, 1  # MXGEMM_B_NK, MXGEMM_B_KN
+KV_BF16, KV_FP8_E4M3 = 0, 1  # MXGEMM_KV_*: a cache's element format
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MXGEMM_NOALLOC_SCRATCH_BYTES
 
 
@@ -90,8 +92,35 @@ class Norm(ctypes.Structure):
                 ("a_format", ctypes.c_int32)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("pages", ctypes.c_void_p),
+                ("ld_pages", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class Append(ctypes.Structure):
+    _fields_ = [("Q", ctypes.c_void_p), ("Q_out", ctypes.c_void_p), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("ldqo", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("factor", ctypes.c_float),
+                ("heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("Q", ctypes.c_void_p), ("O", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("sinks", ctypes.c_void_p),
+                ("A", ctypes.c_void_p), ("scaleA", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("ldo", ctypes.c_int64),
+                ("lda", ctypes.c_int64), ("ldsa", ctypes.c_int64), ("scale", ctypes.c_float), ("heads", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("a_format", ctypes.c_int32)]
+
+
 _pack_grouped = struct.Struct("@7qi4x").pack
 _pack_norm = struct.Struct("@PqPPiiPPqPqffPqPPqPPqqi4x").pack
+_pack_cache = struct.Struct("@PPqqqPqPPPPiiiiiii4x").pack
+_pack_append = struct.Struct("@PPPPqqqqPPfiii").pack
+_pack_attention = struct.Struct("@PPPPPPqqqqfiiiii").pack
 
 _lib = None
 
@@ -137,6 +166,14 @@ def lib():
         L.mxgemm_glu_quantize.restype = i32
         L.mxgemm_norm_quantize.argtypes = [vp, i32, i32, vp]
         L.mxgemm_norm_quantize.restype = i32
+        L.mxgemm_kv_append.argtypes = [vp, vp, i32, vp]
+        L.mxgemm_kv_append.restype = i32
+        L.mxgemm_rope_frequencies.argtypes = [vp, i32] + [ctypes.c_double] * 5
+        L.mxgemm_rope_frequencies.restype = i32
+        L.mxgemm_paged_attention.argtypes = [vp, vp, i32, vp, ctypes.c_size_t, vp]
+        L.mxgemm_paged_attention.restype = i32
+        L.mxgemm_paged_attention_workspace_bytes.argtypes = [i32] * 5
+        L.mxgemm_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         L.mxgemm_query.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
         L.mxgemm_query.restype = i32
         L.mxgemm_plan.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(Info)]
@@ -352,6 +389,57 @@ def mxgemm_norm_quantize(T, K, Y, X=None, H=None, Z=None, A=None, scaleA=None, p
     if check:
         _check(st, "mxgemm_norm_quantize")
     return st
+
+
+def make_kv_cache(k, v, pages, offsets, lens, *, seqs, num_pages, page_size, max_pages, kv_heads, head_dim, fp8=False,
+                  k_scale=None, v_scale=None, ld_pages=None, page_stride=None, head_stride=None, token_stride=None):
+    """A paged cache and its batch for the calls below, as bytes that hold the
+    tensors' addresses (keep the tensors); strides in elements, by default pages
+    of [kv_heads][page_size][head_dim]."""
+    token = head_dim if token_stride is None else token_stride
+    head = page_size * token if head_stride is None else head_stride
+    return _pack_cache(_ptr(k) or 0, _ptr(v) or 0, kv_heads * head if page_stride is None else page_stride, head, token,
+                       _ptr(pages) or 0, max_pages if ld_pages is None else ld_pages, _ptr(offsets) or 0, _ptr(lens) or 0,
+                       _ptr(k_scale) or 0, _ptr(v_scale) or 0, num_pages, page_size, seqs, max_pages, kv_heads, head_dim,
+                       KV_FP8_E4M3 if fp8 else KV_BF16)
+
+
+def mxgemm_kv_append(cache, T, Q=None, K=None, V=None, Q_out=None, heads=0, ldq=0, ldk=0, ldv=0, ldqo=0, positions=None,
+                     freq=None, rot_dim=0, interleaved=False, factor=1.0, stream=None, check=True):
+    """Turn the new tokens' queries and keys to their positions, Q to Q_out, K
+    and V to the cache's pages (asynchronous; cache: make_kv_cache)."""
+    p = _pack_append(_ptr(Q) or 0, _ptr(Q_out) or 0, _ptr(K) or 0, _ptr(V) or 0, ldq, ldqo, ldk, ldv, _ptr(positions) or 0,
+                     _ptr(freq) or 0, factor, heads, rot_dim, interleaved)
+    st = lib().mxgemm_kv_append(cache, p, int(T), _stream(stream))
+    if check:
+        _check(st, "mxgemm_kv_append")
+    return st
+
+
+def mxgemm_rope_frequencies(rot_dim, base=10000.0, factor=1.0, original=0.0, low=0.0, high=0.0) -> list:
+    """The rot_dim / 2 frequencies of mxgemm_kv_append, float64 values on the host."""
+    freq = (ctypes.c_double * max(rot_dim // 2, 1))()
+    _check(lib().mxgemm_rope_frequencies(freq, int(rot_dim), float(base), float(factor), float(original), float(low),
+                                         float(high)), "mxgemm_rope_frequencies")
+    return list(freq)
+
+
+def mxgemm_paged_attention(cache, T, Q, O=None, *, heads, scale, workspace, workspace_bytes, lse=None, sinks=None, A=None,
+                           scaleA=None, ldq=0, ldo=0, lda=0, ldsa=0, causal=True, window=0, max_new=0, a_format=FMT_FP4,
+                           stream=None, check=True):
+    """Attention of the new tokens' Q over the cache (asynchronous; bf16 O and /
+    or the quantized A and scaleA; workspace: zeroed once,
+    mxgemm_paged_attention_workspace_bytes)."""
+    p = _pack_attention(_ptr(Q) or 0, _ptr(O) or 0, _ptr(lse) or 0, _ptr(sinks) or 0, _ptr(A) or 0, _ptr(scaleA) or 0, ldq,
+                        ldo, lda, ldsa, scale, heads, causal, window, max_new, a_format)
+    st = lib().mxgemm_paged_attention(cache, p, int(T), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(st, "mxgemm_paged_attention")
+    return st
+
+
+def mxgemm_paged_attention_workspace_bytes(T, seqs, heads, kv_heads, head_dim) -> int:
+    return int(lib().mxgemm_paged_attention_workspace_bytes(int(T), int(seqs), int(heads), int(kv_heads), int(head_dim)))
 
 
 def mxgemm_query(M, N, K, b_packed=0, split_k=-1) -> dict:

@@ -1,0 +1,63 @@
+// Arguments and launchers of the attention kernels over a paged cache (append
+// with rotary positions, attention of new tokens).  Host-side only plain
+// types; no device code.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mx {
+
+// A paged cache and the batch that uses it (strides in bytes).
+struct CacheArgs {
+    uint8_t *k, *v;
+    int64_t page_b, head_b, token_b;
+    const int32_t *pages;    // [seqs][ld_pages]
+    int64_t ld_pages;
+    const int32_t *offsets;  // [seqs + 1]
+    const int32_t *lens;     // [seqs]
+    const float *k_scale, *v_scale;  // [kv_heads] or null
+    int num_pages, page_shift, seqs, max_pages, kv_heads;
+    int D;
+};
+
+// ---- append (mx_append.hip)
+struct AppendArgs {
+    CacheArgs c;
+    const uint16_t *Q, *K, *V;  // bf16 rows; Q, or K and V, may be null
+    uint16_t *QO;
+    int64_t ldq, ldk, ldv, ldqo;
+    const int32_t *positions;   // [T] or null
+    const double *freq;         // [rot / 2], radians a position
+    float factor;
+    int T, heads, rot, interleaved, fp8;
+};
+void launch_append(const AppendArgs &a, int num_cu, hipStream_t s);
+
+// ---- attention
+constexpr int kAttnTile = 32;    // rows (token, head of a group) that a wave holds
+constexpr int kAttnGroup = 128;  // keys that work is handed out by
+constexpr int kAttnPieces = 512; // workgroups that may leave partial results, at most
+constexpr int kAttnCounterBytes = 4096;
+struct AttnArgs {
+    CacheArgs c;
+    const uint16_t *Q;
+    uint16_t *O;             // bf16 [T][ldo] or null
+    float *lse;              // [T][heads] or null
+    uint8_t *A, *S;          // quantized rows or null
+    const float *sinks;      // [heads] or null
+    int64_t ldq, ldo, lda_b, lds;
+    float scale;
+    int T, heads, group;     // group: query heads of a key head
+    int causal, window, a_fp8;
+    int *counters;           // [kAttnPieces], zero between calls
+    float *partials;
+};
+// The kernel whose waves take keys in turn (mx_attn_keys.hip).  Its workgroups
+// per compute unit, and the floats of a partial result.
+int attn_keys_per_cu(int D, bool fp8);
+int64_t attn_partial_floats(int D);
+void launch_attn_keys(const AttnArgs &a, bool fp8, int grid, hipStream_t s);
+
+}  // namespace mx

@@ -1,0 +1,508 @@
+// Device code that the attention kernels share: a sequence's extents, keys and
+// values from pages into LDS, the products with a block of 32 keys, the
+// running softmax, and what is done with a finished row.
+//
+// One wave holds 32 rows of queries (a row is one new token and one of the
+// query heads that share a key head) and takes 32 keys at a time:
+//
+//   S^T[key][row] = K Q^T     v_mfma_f32_32x32x16_bf16, K first, Q second
+//   O^T[d][row]  += V^T P^T   the same, V^T first, P^T second
+//
+// Both products have the row in the lane: lane l holds row l % 32, and of a
+// block's 32 keys those with (key / 4) % 2 = l / 32 (accumulator g: key
+// 8 (g / 4) + 4 (l / 32) + g % 4).  So the softmax of a row needs one exchange
+// (the two lanes of a row), its maximum and sum are one register each, and P
+// is the second product's operand where it stands: the order of the keys
+// within a product's 16 is free as long as both operands have it, and V^T is
+// read from LDS in P's order (transposed reads, whose rows each lane names).
+//
+// The scores are scaled by c = scale * k_scale * log2(e), p = 2^(c s - m).
+// P is rounded to bf16 for the second product (2^-9 of each p, which leaves
+// the result about as far off as its own rounding to bf16 does); the sum adds
+// the unrounded p in fp32.  The running maximum is raised only where it grows
+// by more than 8 (p up to 2^8): all of O would have to be rescaled otherwise.
+#pragma once
+
+#include "mx_attention.hpp"
+#include "mx_pipe.hpp"
+#include "mx_quantize_out.hpp"
+
+namespace mx {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kRaise = 8.0f;
+
+template <int N>
+__device__ __forceinline__ void attn_wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int OFF>
+__device__ __forceinline__ v2u lds_read_tr16(uint32_t base)
+{
+    static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+    v2u r;
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(r) : "v"(base), "n"(OFF) : "memory");
+    return r;
+}
+
+template <int OFF>
+__device__ __forceinline__ v2u lds_read_tr8(uint32_t base)
+{
+    static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+    v2u r;
+    asm volatile("ds_read_b64_tr_b8 %0, %1 offset:%2" : "=v"(r) : "v"(base), "n"(OFF) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ v16f mfma32(v4i a, v4i b, v16f c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// 8 E4M3 codes to 8 bf16 (exact)
+__device__ __forceinline__ v4i bf16_of_fp8(v2u w)
+{
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = __builtin_bit_cast(int, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], 1.0f, true)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], 1.0f, false));
+    return r;
+}
+
+// A value of the two lanes of a row combined
+__device__ __forceinline__ float row_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float row_sum(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Read-only data at a wave-uniform address: scalar loads, also after asm that
+// the compiler takes for a store.
+__device__ __forceinline__ int load_uniform(const int32_t *p)
+{
+    return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+}
+__device__ __forceinline__ float load_uniform(const float *p)
+{
+    return *(const __attribute__((address_space(4))) float *)(uintptr_t)p;
+}
+
+// ---- sequences
+
+struct AttnSeq {
+    int t0, n, len;  // first new token, new tokens, keys (whatever the arrays hold: within T and the page table)
+};
+
+__device__ __forceinline__ AttnSeq seq_from(const CacheArgs &c, int T, int o0, int o1, int len)
+{
+    o0 = min(max(o0, 0), T);
+    o1 = min(max(o1, 0), T);
+    return {o0, max(o1 - o0, 0), min(max(len, 0), c.max_pages << c.page_shift)};
+}
+
+// s wave-uniform
+__device__ __forceinline__ AttnSeq load_seq(const CacheArgs &c, int T, int s)
+{
+    return seq_from(c, T, load_uniform(c.offsets + s), load_uniform(c.offsets + s + 1), load_uniform(c.lens + s));
+}
+
+// Rows of a sequence, in tiles of `tile`; and the 128-key groups that a tile
+// can need (an upper bound where a window moves with the tokens)
+__device__ __forceinline__ int seq_tiles(const AttnSeq &q, int group, int tile) { return (q.n * group + tile - 1) / tile; }
+__device__ __forceinline__ int seq_groups(const AttnSeq &q, int group, int tile, int window)
+{
+    int n = (q.len + kAttnGroup - 1) / kAttnGroup;
+    if (window > 0) {
+        const int64_t most = (int64_t)window + tile / group + 1;
+        n = (int)min((int64_t)n, (most + kAttnGroup - 1) / kAttnGroup + 1);
+    }
+    return max(n, 1);
+}
+
+// Keys [lo, hi) that the tokens i0 .. i1 of a sequence can see between them
+__device__ __forceinline__ void tile_keys(const AttnArgs &a, const AttnSeq &q, int i0, int i1, int &lo, int &hi)
+{
+    const int p0 = q.len - q.n + i0, p1 = q.len - q.n + i1;
+    hi = a.causal ? min(max(p1 + 1, 0), q.len) : (p1 < 0 ? 0 : q.len);
+    lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+    lo = min(lo, hi);
+}
+
+// ---- keys and values in LDS
+//
+// A row of DP elements is ROWB bytes of 16-byte chunks; load instructions fill
+// 1 KiB, whole rows, so a chunk's place within its row is chosen by which
+// chunk a lane loads.  K rows: chunk c at c ^ kswz(row): the 16 rows that a
+// 16-byte read serves in one cycle fall on different banks.  V rows: 64-byte
+// (bf16) or 32-byte (8 bits) pieces, piece p at p ^ vswz(row): a transposed
+// read serves 4 rows x 64 bytes, or 8 rows x 32 bytes, at a time.
+template <int DP, bool FP8>
+struct AttnLds {
+    static constexpr int ROWB = DP * (FP8 ? 1 : 2);
+    static constexpr int CH = ROWB / 16;       // chunks of a row
+    static constexpr int RPI = 1024 / ROWB;    // rows of a load instruction
+    static constexpr int NIH = 16 / RPI;       // load instructions of 16 keys
+    static constexpr int BLOCK = 32 * ROWB;    // 32 keys
+    static constexpr int NS = DP / 16;         // products over d
+    static constexpr int ND = DP / 32;         // blocks of O's columns
+    static_assert(RPI >= 1 && NIH >= 1, "rows of 64 to 512 bytes");
+
+    static __device__ __forceinline__ int kswz(int r)
+    {
+        return ROWB >= 256 ? r & 15 : ROWB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+    }
+    static __device__ __forceinline__ int vswz(int r)
+    {
+        if constexpr (FP8)
+            return ROWB >= 256 ? (r & 3) | ((r >> 1) & 4) : ROWB == 128 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r >> 3) & 1;
+        else
+            return ROWB >= 256 ? r & 3 : (r >> 1) & 1;
+    }
+    // chunk that stands at place c of row r
+    static __device__ __forceinline__ int k_chunk(int r, int c) { return c ^ kswz(r); }
+    static __device__ __forceinline__ int v_chunk(int r, int c) { return c ^ (vswz(r) * (FP8 ? 2 : 4)); }
+
+    // this lane's byte offsets in 16 rows of the cache, by load instruction
+    // (columns from D on lie outside every page: zeros)
+    static __device__ __forceinline__ void load_offsets(const CacheArgs &c, int lane, uint32_t (&ko)[NIH], uint32_t (&vo)[NIH])
+    {
+        const int place = lane % CH;
+#pragma unroll
+        for (int j = 0; j < NIH; ++j) {
+            const int r = j * RPI + lane / CH;
+            const int kc = k_chunk(r, place) * 16, vc = v_chunk(r, place) * 16;
+            const int row = c.D * (FP8 ? 1 : 2);
+            ko[j] = kc < row ? (uint32_t)(r * c.token_b + kc) : kOOB;
+            vo[j] = vc < row ? (uint32_t)(r * c.token_b + vc) : kOOB;
+        }
+    }
+
+    // LDS addresses of this lane's K fragments of a block (bf16: product s,
+    // columns 16 s + 8 (lane / 32) + 0..7; 8 bits: products 2 p and 2 p + 1,
+    // columns 16 (2 p + lane / 32) + 0..7 and + 8..15)
+    static constexpr int KF = FP8 ? NS / 2 : NS;
+    static __device__ __forceinline__ void k_addr(uint32_t base, int lane, uint32_t (&ka)[KF])
+    {
+        const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int s = 0; s < KF; ++s)
+            ka[s] = base + r * ROWB + ((2 * s + h) ^ kswz(r)) * 16;
+    }
+    // ... and of its V^T fragments, by block of 32 columns
+    static __device__ __forceinline__ void v_addr(uint32_t base, int lane, uint32_t (&va)[ND])
+    {
+        const int h = lane >> 5, grp = (lane >> 4) & 1, q = lane & 15;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            if constexpr (FP8) {
+                const int i = q >> 1, r = (i >> 2) * 8 + 4 * h + (i & 3);
+                va[d] = base + r * ROWB + (d ^ vswz(r)) * 32 + grp * 16 + (q & 1) * 8;
+            } else {
+                const int r = 4 * h + (q >> 2);
+                va[d] = base + r * ROWB + (d ^ vswz(r)) * 64 + grp * 32 + (q & 3) * 8;
+            }
+        }
+    }
+    // columns of this lane's Q fragment s
+    static __device__ __forceinline__ int q_col(int s, int lane)
+    {
+        const int h = lane >> 5;
+        return FP8 ? 16 * (2 * (s >> 1) + h) + 8 * (s & 1) : 16 * s + 8 * h;
+    }
+};
+
+// 16 keys from key0 on of one key head: descriptors of K's and V's rows that
+// exist (the others read as zeros).  page: the page's index as the table has it.
+struct AttnRows {
+    __amdgpu_buffer_rsrc_t k, v;
+};
+__device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, int head, int page, int key0, int len)
+{
+    const bool there = (uint32_t)page < (uint32_t)c.num_pages;
+    const int rows = there ? min(max(len - key0, 0), 16) : 0;
+    const int64_t at = (int64_t)(there ? page : 0) * c.page_b + head * c.head_b +
+                       (int64_t)(key0 & ((1 << c.page_shift) - 1)) * c.token_b;
+    const uint32_t bytes = (uint32_t)rows * (uint32_t)c.token_b;
+    return {make_rsrc_u(c.k + at, bytes), make_rsrc_u(c.v + at, bytes)};
+}
+__device__ __forceinline__ int attn_page(const CacheArgs &c, const int32_t *table, int key0)
+{
+    return load_uniform(table + min(key0 >> c.page_shift, c.max_pages - 1));
+}
+
+// ---- products and softmax
+
+// This lane's Q fragments (its row's columns), negated where the scores' scale
+// is negative; zeros for rows and columns that do not exist.
+template <int DP, bool FP8>
+__device__ __forceinline__ void load_q(const AttnArgs &a, const uint16_t *row, bool live, bool negate, int lane,
+                                       v4i (&q)[DP / 16])
+{
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+        const int col = AttnLds<DP, FP8>::q_col(s, lane);
+        q[s] = v4i{0, 0, 0, 0};
+        if (live && col < a.c.D)
+            q[s] = *reinterpret_cast<const v4i *>(row + col);
+        if (negate)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                q[s][i] ^= (int)0x80008000;
+    }
+}
+
+// S^T of one block of 32 keys in LDS
+template <int DP, bool FP8>
+__device__ __forceinline__ v16f scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF], uint32_t at, const v4i (&q)[DP / 16])
+{
+    using L = AttnLds<DP, FP8>;
+    v16f s = {};
+    constexpr int B = L::KF < 8 ? L::KF : 8;  // fragments read together
+    static_for<L::KF / B>([&](auto bc) {
+        v4i f[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            f[i] = lds_read16<0>(ka[bc.value * B + i] + at);
+        static_for<B / 2>([&](auto ic) {
+            constexpr int I = 2 * ic.value;
+            lds_wait_n<B - I - 2>(f[I], f[I + 1]);
+#pragma unroll
+            for (int i = I; i < I + 2; ++i) {
+                const int n = bc.value * B + i;
+                if constexpr (FP8) {
+                    s = mfma32(bf16_of_fp8(v2u{(uint32_t)f[i][0], (uint32_t)f[i][1]}), q[2 * n], s);
+                    s = mfma32(bf16_of_fp8(v2u{(uint32_t)f[i][2], (uint32_t)f[i][3]}), q[2 * n + 1], s);
+                } else {
+                    s = mfma32(f[i], q[n], s);
+                }
+            }
+        });
+    });
+    return s;
+}
+
+// The running softmax's state of this lane's row
+template <int ND>
+struct AttnState {
+    float m, l;  // maximum so far (of both lanes of the row), sum (this lane's keys)
+    v16f o[ND];
+    __device__ __forceinline__ void reset()
+    {
+        m = kNegInf;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            o[d] = v16f{};
+    }
+};
+
+// Scores to P (bf16 pairs, the second product's operands for its two steps of
+// 16 keys), raising the maximum where it has to be.
+template <int ND>
+__device__ __forceinline__ void softmax_block(AttnState<ND> &t, v16f s, float c, v4i (&p)[2])
+{
+    float x = fmaxf(s[0], s[1]);
+#pragma unroll
+    for (int g = 2; g < 16; ++g)
+        x = fmaxf(x, s[g]);
+    x = row_max(x) * c;
+    if (__builtin_amdgcn_ballot_w64(x > t.m + kRaise)) {
+        const float m = fmaxf(t.m, x);
+        const float w = m == kNegInf ? 1.0f : exp2_fast(t.m - m);
+        t.m = m;
+        t.l *= w;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+                t.o[d][g] *= w;
+    }
+    // a row that has seen no key yet: every score is -inf, p = 0
+    const float m = t.m == kNegInf ? 0.0f : t.m;
+    float e[16];
+#pragma unroll
+    for (int g = 0; g < 16; ++g)
+        e[g] = exp2_fast(fmaf(s[g], c, -m));
+    float sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sum[i] = (e[4 * i] + e[4 * i + 1]) + (e[4 * i + 2] + e[4 * i + 3]);
+    t.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        p[i >> 2][i & 3] = (int)bf16x2_rne(e[2 * i], e[2 * i + 1]);
+}
+
+// V^T fragments of columns 32 d .. 32 d + 31, keys' step s (16 keys)
+template <int DP, bool FP8>
+struct AttnV {
+    using L = AttnLds<DP, FP8>;
+    v2u r[FP8 ? 1 : 2];
+    template <int S>
+    __device__ __forceinline__ void read(uint32_t at)
+    {
+        if constexpr (FP8) {
+            r[0] = lds_read_tr8<S * 16 * L::ROWB>(at);
+        } else {
+            r[0] = lds_read_tr16<S * 16 * L::ROWB>(at);
+            r[1] = lds_read_tr16<(S * 16 + 8) * L::ROWB>(at);
+        }
+    }
+    static constexpr int N = FP8 ? 1 : 2;  // reads
+    __device__ __forceinline__ v4i frag() const
+    {
+        if constexpr (FP8)
+            return bf16_of_fp8(r[0]);
+        else
+            return v4i{(int)r[0][0], (int)r[0][1], (int)r[1][0], (int)r[1][1]};
+    }
+};
+
+// whether a pair of bf16 holds an infinity or a NaN
+__device__ __forceinline__ bool special_pair(int w)
+{
+    return (w & 0x7F80) == 0x7F80 || (w & 0x7F800000) == 0x7F800000;
+}
+
+// The products with V^T where it holds infinities or NaN and some rows do not
+// see all keys: key by key, added to the rows that see it (0 times an infinity
+// is a NaN: a p of 0 does not keep it out).
+__device__ __forceinline__ v16f values_apart(const v4i (&w)[2], const v4i (&p)[2], int lo, int hi, int lane)
+{
+    v16f sum = {};
+#pragma unroll 1
+    for (int key = 0; key < 32; ++key) {
+        // the key's slot: step key / 16, lane half (key / 4) % 2, element 4 ((key / 8) % 2) + key % 4
+        const int e = 4 * ((key >> 3) & 1) + (key & 3);
+        const int keep = ((key >> 2) & 1) == (lane >> 5) ? 0xFFFF << (16 * (e & 1)) : 0;
+        v4i w1, p1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = i == (e >> 1) ? keep : 0;
+            w1[i] = (key < 16 ? w[0][i] : w[1][i]) & k;
+            p1[i] = (key < 16 ? p[0][i] : p[1][i]) & k;
+        }
+        const v16f x = mfma32(w1, p1, v16f{});
+        const bool sees = key >= lo && key < hi;
+#pragma unroll
+        for (int g = 0; g < 16; ++g)
+            sum[g] += sees ? x[g] : 0.0f;
+    }
+    return sum;
+}
+
+// O^T += V^T P^T of one block.  masked (wave-uniform): some rows do not see
+// some of its keys; lo, hi: keys of the block that this lane's row sees.
+template <int DP, bool FP8>
+__device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND], uint32_t at, const v4i (&p)[2],
+                                       AttnState<AttnLds<DP, FP8>::ND> &t, bool masked, int lo, int hi, int lane)
+{
+    using L = AttnLds<DP, FP8>;
+    using V = AttnV<DP, FP8>;
+    constexpr int B = 2;  // blocks of columns read together
+    static_for<L::ND / B>([&](auto bc) {
+        constexpr int D0 = bc.value * B;
+        V f[B][2];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            f[i][0].template read<0>(va[D0 + i] + at);
+            f[i][1].template read<1>(va[D0 + i] + at);
+        }
+        static_for<B>([&](auto ic) {
+            constexpr int I = ic.value;
+            lds_wait_n<(B - 1 - I) * 2 * V::N>(f[I][0].r, f[I][1].r);
+            v4i w[2] = {f[I][0].frag(), f[I][1].frag()};
+            if (masked) {
+                bool special = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    special |= special_pair(w[e >> 2][e & 3]);
+                if (__builtin_amdgcn_ballot_w64(special)) {
+                    const v16f x = values_apart(w, p, lo, hi, lane);
+#pragma unroll
+                    for (int g = 0; g < 16; ++g)
+                        t.o[D0 + I][g] += x[g];
+                    w[0] = w[1] = v4i{0, 0, 0, 0};
+                }
+            }
+            t.o[D0 + I] = mfma32(w[0], p[0], t.o[D0 + I]);
+            t.o[D0 + I] = mfma32(w[1], p[1], t.o[D0 + I]);
+        });
+    });
+}
+
+// Scores outside a row's keys to -inf.  lo, hi: relative to the block.
+__device__ __forceinline__ void mask_scores(v16f &s, int lo, int hi, int lane)
+{
+    const int h = 4 * (lane >> 5);
+#pragma unroll
+    for (int g = 0; g < 16; ++g) {
+        const int key = 8 * (g >> 2) + h + (g & 3);
+        s[g] = key >= lo && key < hi ? s[g] : kNegInf;
+    }
+}
+
+// The scale of a key head's scores, as a positive factor (in powers of two),
+// whether Q is to be negated for it, and whether it is 0 (Q is then taken as
+// 0 with a factor of 1: masked scores, -inf, must not meet a factor of 0).
+struct AttnScale {
+    float c;
+    bool negate, zero;
+};
+__device__ __forceinline__ AttnScale attn_scale(const AttnArgs &a, int head)
+{
+    const float c = a.scale * kLog2e * (a.c.k_scale ? load_uniform(a.c.k_scale + head) : 1.0f);
+    return {c == 0.0f ? 1.0f : fabsf(c), c < 0.0f, c == 0.0f};
+}
+
+// A finished row's 8 columns from col on: o relative to 2^m, l the sum; the
+// sink's share joins the sum.  Every lane of a quad has the same row.
+template <typename F>
+__device__ __forceinline__ void finish_row(const AttnArgs &a, int kv_head, int token, int head, int col, float m, float l,
+                                           F &&o, bool live)
+{
+    float w = 1.0f;
+    if (a.sinks) {
+        const float k = a.sinks[head] * kLog2e, n = fmaxf(m, k);
+        if (n != kNegInf) {
+            w = exp2_fast(m - n);
+            l = l * w + exp2_fast(k - n);
+            m = n;
+        }
+    }
+    const float vs = a.c.v_scale ? a.c.v_scale[kv_head] : 1.0f;
+    const float f = l == 0.0f ? 0.0f : w / l * vs;
+    v4i x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = (int)bf16x2_rne(o(2 * i) * f, o(2 * i + 1) * f);
+    if (live && a.O)
+        *reinterpret_cast<v4i *>(a.O + (int64_t)token * a.ldo + head * a.c.D + col) = x;
+    if (live && a.lse && col == 0)
+        a.lse[(int64_t)token * a.heads + head] = l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.A) {
+        uint8_t *A = a.A + (int64_t)token * a.lda_b, *S = a.S + (int64_t)token * a.lds;
+        if (a.a_fp8)
+            quantize_store<true>(x, A, S, head * a.c.D + col, live);
+        else
+            quantize_store<false>(x, A, S, head * a.c.D + col, live);
+    }
+}
+
+}  // namespace mx

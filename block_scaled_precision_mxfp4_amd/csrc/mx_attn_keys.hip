@@ -1,0 +1,271 @@
+// Attention of few rows per key head (decode, short chunks): the waves of a
+// workgroup share a tile of 32 rows and take its keys 32 at a time in turn, so
+// that a long context is spread over every wave of the card.  Bound by HBM:
+// every key and value is read once.
+//
+// Each wave has a ring of its own in LDS, filled by direct-to-LDS loads of
+// whole rows (pages are found by scalar loads, a page's descriptor ends with
+// the sequence), and waits for nothing but its own loads: no barrier until the
+// waves' results are merged.  The rings hold up to 128 KiB of a compute
+// unit's loads in flight (8 TB/s for about 2 us need 60 KiB).
+#include "mx_attn_plan.hpp"
+
+namespace mx {
+
+namespace {
+
+// waves of a workgroup and slots of a wave's ring: the most that fit 128 KiB
+// (64 KiB where two workgroups then share a compute unit)
+template <int DP, bool FP8>
+struct KeysShape {
+    static constexpr int STAGE = 2 * AttnLds<DP, FP8>::BLOCK;
+    static constexpr int NW = STAGE > 16384 ? 2 : 4;
+    static constexpr int ST = STAGE > 8192 ? 2 : 4;
+    static constexpr int BYTES = NW * ST * STAGE;
+    static constexpr int PER_CU = BYTES <= 65536 ? 2 : 1;
+};
+
+template <int DP, bool FP8>
+__global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_kernel(AttnArgs a)
+{
+    using L = AttnLds<DP, FP8>;
+    using SH = KeysShape<DP, FP8>;
+    constexpr int NW = SH::NW, ST = SH::ST, STAGE = SH::STAGE;
+    constexpr int NI = 2 * L::NIH;        // load instructions of a block of K, or of V
+    constexpr int GB = kAttnGroup / 32;   // blocks of a group
+    constexpr int QC = DP / 8;            // 8-column pieces of a row
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
+    __shared__ float s_ml[NW][32][2];
+    __shared__ int s_last;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wg = blockIdx.x;
+    AttnPlan plan;
+    int chunk;
+    if (!attn_plan(a, kAttnTile, wg, gridDim.x, lane, plan, chunk))
+        return;
+
+    uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
+    L::load_offsets(a.c, lane, ko, vo);
+    uint8_t *mine = ring + wave * (ST * STAGE);
+    L::k_addr(lds_addr(mine), lane, ka);
+    L::v_addr(lds_addr(mine) + L::BLOCK, lane, va);
+
+    int at = wg * chunk;
+    const int end = min(at + chunk, plan.total);
+    int s = plan.s, seq_start = plan.start;
+    AttnSeq q = load_seq(a.c, a.T, s);
+    int cost = seq_groups(q, a.group, kAttnTile, a.window);
+    int units = seq_tiles(q, a.group, kAttnTile) * a.c.kv_heads;
+    while (at < end) {
+        while (at >= seq_start + units * cost) {  // (the line's end is a sequence's: this stops before the last one)
+            seq_start += units * cost;
+            if (++s >= a.c.seqs)
+                return;
+            q = load_seq(a.c, a.T, s);
+            cost = seq_groups(q, a.group, kAttnTile, a.window);
+            units = seq_tiles(q, a.group, kAttnTile) * a.c.kv_heads;
+        }
+        const int u = (at - seq_start) / cost;
+        const int unit_start = seq_start + u * cost;
+        const int tile = u / a.c.kv_heads, head = u % a.c.kv_heads;
+        const int piece_end = min(end, unit_start + cost);
+        // its rows, and the keys that they see
+        const int r0 = tile * kAttnTile, rows = min(q.n * a.group - r0, kAttnTile);
+        int lo, hi;
+        tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
+        const int g0 = lo / kAttnGroup;
+        const int b0 = max((g0 + at - unit_start) * GB, lo / 32), b1 = min((g0 + piece_end - unit_start) * GB, (hi + 31) / 32);
+        const int nb = max((b1 - b0 - wave + NW - 1) / NW, 0);  // this wave's blocks: b0 + wave, + NW, ...
+
+        const int32_t *table = a.c.pages + (int64_t)s * a.c.ld_pages;
+        auto issue = [&](int i, int pg0, int pg1) __attribute__((always_inline)) {
+            const int key0 = (b0 + wave + i * NW) * 32, len = i < nb ? q.len : 0;
+            const AttnRows x = attn_rows(a.c, head, pg0, key0, len), y = attn_rows(a.c, head, pg1, key0 + 16, len);
+            uint8_t *to = mine + (i % ST) * STAGE;
+#pragma unroll
+            for (int j = 0; j < L::NIH; ++j)
+                load16_to_lds_stream(x.k, (lds_void *)(to + j * 1024), ko[j]);
+#pragma unroll
+            for (int j = 0; j < L::NIH; ++j)
+                load16_to_lds_stream(y.k, (lds_void *)(to + L::BLOCK / 2 + j * 1024), ko[j]);
+#pragma unroll
+            for (int j = 0; j < L::NIH; ++j)
+                load16_to_lds_stream(x.v, (lds_void *)(to + L::BLOCK + j * 1024), vo[j]);
+#pragma unroll
+            for (int j = 0; j < L::NIH; ++j)
+                load16_to_lds_stream(y.v, (lds_void *)(to + L::BLOCK + L::BLOCK / 2 + j * 1024), vo[j]);
+        };
+        auto pages = [&](int i, int &pg0, int &pg1) __attribute__((always_inline)) {
+            const int key0 = (b0 + wave + i * NW) * 32;
+            pg0 = attn_page(a.c, table, key0);
+            pg1 = attn_page(a.c, table, key0 + 16);
+        };
+
+        AttnState<L::ND> t;
+        t.reset();
+        const AttnScale sc = attn_scale(a, head);
+        const int row = lane & 31;
+        const int idx = (r0 + min(row, rows - 1)) / a.group;  // the row's new token
+        const int pos = q.len - q.n + idx;
+        const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
+        const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        if (nb > 0) {
+            int pg0, pg1;
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i) {
+                pages(i, pg0, pg1);
+                issue(i, pg0, pg1);
+            }
+            pages(ST - 1, pg0, pg1);
+            v4i qf[L::NS];
+            {
+                const int hq = head * a.group + (r0 + row) % a.group;
+                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + hq * a.c.D, row < rows && !sc.zero, sc.negate, lane,
+                                qf);
+            }
+            // keys that every row of the tile sees
+            const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 31) : 0;
+            const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
+            for (int i = 0; i < nb; ++i) {
+                issue(i + ST - 1, pg0, pg1);
+                pages(i + ST, pg0, pg1);
+                const uint32_t slot = (uint32_t)((i % ST) * STAGE);
+                const int key0 = (b0 + wave + i * NW) * 32;
+                attn_wait_vm<NI + (ST - 1) * 2 * NI>();
+                v16f x = scores<DP, FP8>(ka, slot, qf);
+                const bool masked = key0 < all_lo || key0 + 32 > all_hi;
+                if (masked)
+                    mask_scores(x, row_lo - key0, row_hi - key0, lane);
+                v4i p[2];
+                softmax_block(t, x, sc.c, p);
+                attn_wait_vm<(ST - 1) * 2 * NI>();
+                values<DP, FP8>(va, slot, p, t, masked, row_lo - key0, row_hi - key0, lane);
+            }
+        }
+        // merge the waves: O to the wave's ring, rows of DP floats whose
+        // 16-byte chunks are swizzled by the row
+        attn_wait_vm<0>();
+        t.l = row_sum(t.l);
+        if (row < rows) {
+            float *o = reinterpret_cast<float *>(mine) + row * DP;
+#pragma unroll
+            for (int d = 0; d < L::ND; ++d)
+#pragma unroll
+                for (int g = 0; g < 16; g += 4) {
+                    const int ch = d * 8 + (g >> 2) * 2 + (lane >> 5);
+                    *reinterpret_cast<v4f *>(o + ((ch ^ (row & 15)) * 4)) = v4f{t.o[d][g], t.o[d][g + 1], t.o[d][g + 2], t.o[d][g + 3]};
+                }
+            if (lane < 32) {
+                s_ml[wave][row][0] = t.m;
+                s_ml[wave][row][1] = t.l;
+            }
+        }
+        __syncthreads();
+        // the unit's workgroups (at most one unit that goes on behind a workgroup
+        // starts in it: its counter is that workgroup's), and this one's place for
+        // a partial result
+        const int first = unit_start / chunk, last = (unit_start + cost - 1) / chunk;
+        const bool whole = first == last;
+        const int64_t floats = 32 * (DP + 2);
+        float *part = a.partials + (2 * (int64_t)wg + (unit_start > wg * chunk ? 1 : 0)) * floats;
+        for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
+            const int r = it / QC, c8 = it % QC;
+            const bool live = r < rows && c8 * 8 < a.c.D;
+            const int rr = min(r, rows - 1);
+            float m = kNegInf, l = 0.0f, o[8] = {};
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                m = fmaxf(m, s_ml[w][rr][0]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = m == kNegInf ? 1.0f : exp2_fast(s_ml[w][rr][0] - m);
+                l += f * s_ml[w][rr][1];
+                const float *src = reinterpret_cast<const float *>(ring + w * (ST * STAGE)) + rr * DP;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const v4f x = *reinterpret_cast<const v4f *>(src + (((2 * c8 + h) ^ (rr & 15)) * 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[4 * h + e] += f * x[e];
+                }
+            }
+            if (whole) {
+                const int i = (r0 + rr) / a.group;
+                finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
+            } else if (live) {
+                const __amdgpu_buffer_rsrc_t to = make_rsrc_u(part, (uint32_t)(floats * 4));
+                store16_coherent(to, (uint32_t)((r * DP + c8 * 8) * 4), v4f{o[0], o[1], o[2], o[3]});
+                store16_coherent(to, (uint32_t)((r * DP + c8 * 8 + 4) * 4), v4f{o[4], o[5], o[6], o[7]});
+                if (c8 == 0)
+                    __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(m), __float_as_uint(l)}, to,
+                                                          (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
+            }
+        }
+        if (!whole && split_arrive_last_via(a.counters + first, last - first + 1, &s_last)) {
+            // the first workgroup's part of this unit is its last, unless the
+            // unit starts with it; the others' is their first
+            const __amdgpu_buffer_rsrc_t all = make_rsrc_u(a.partials + 2 * (int64_t)first * floats,
+                                                           (uint32_t)((last - first + 1) * 2 * floats * 4));
+            const int off = unit_start > first * chunk ? 1 : 0;
+            for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
+                const int r = it / QC, c8 = it % QC;
+                const bool live = r < rows && c8 * 8 < a.c.D;
+                const int rr = min(r, rows - 1);
+                float m = kNegInf, l = 0.0f, o[8] = {};
+                for (int w = 0; w <= last - first; ++w) {
+                    const uint32_t base = (uint32_t)((2 * w + (w == 0 ? off : 0)) * floats * 4);
+                    const v2u ml = __builtin_amdgcn_raw_buffer_load_b64(all, base + (32 * DP + 2 * rr) * 4, 0, kCoherent);
+                    const v4f x0 = load16_coherent(all, base + (uint32_t)((rr * DP + c8 * 8) * 4));
+                    const v4f x1 = load16_coherent(all, base + (uint32_t)((rr * DP + c8 * 8 + 4) * 4));
+                    const float mw = __uint_as_float(ml[0]), n = fmaxf(m, mw);
+                    const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
+                    m = n;
+                    l = l * f0 + __uint_as_float(ml[1]) * f1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = o[e] * f0 + x0[e] * f1;
+                        o[4 + e] = o[4 + e] * f0 + x1[e] * f1;
+                    }
+                }
+                const int i = (r0 + rr) / a.group;
+                finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
+            }
+        }
+        __syncthreads();  // the rings and s_ml are free again
+        at = piece_end;
+    }
+}
+
+template <int DP, bool FP8>
+void launch(const AttnArgs &a, int grid, hipStream_t s)
+{
+    mx_attn_keys_kernel<DP, FP8><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a);
+}
+
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+}  // namespace
+
+int64_t attn_partial_floats(int D) { return 32 * ((int64_t)padded(D) + 2); }
+
+int attn_keys_per_cu(int D, bool fp8)
+{
+    switch (padded(D)) {
+    case 64: return fp8 ? KeysShape<64, true>::PER_CU : KeysShape<64, false>::PER_CU;
+    case 128: return fp8 ? KeysShape<128, true>::PER_CU : KeysShape<128, false>::PER_CU;
+    default: return fp8 ? KeysShape<256, true>::PER_CU : KeysShape<256, false>::PER_CU;
+    }
+}
+
+void launch_attn_keys(const AttnArgs &a, bool fp8, int grid, hipStream_t s)
+{
+    switch (padded(a.c.D)) {
+    case 64: return fp8 ? launch<64, true>(a, grid, s) : launch<64, false>(a, grid, s);
+    case 128: return fp8 ? launch<128, true>(a, grid, s) : launch<128, false>(a, grid, s);
+    default: return fp8 ? launch<256, true>(a, grid, s) : launch<256, false>(a, grid, s);
+    }
+}
+
+}  // namespace mx

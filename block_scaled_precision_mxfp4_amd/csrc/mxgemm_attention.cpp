@@ -1,0 +1,205 @@
+// C-ABI entry points of the attention over a paged cache declared in
+// libmxgemm.h: argument validation on the host, then one launch on the
+// caller's stream.  Nothing here allocates or keeps state.
+#include "libmxgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mx_attention.hpp"
+#include "mx_host.hpp"
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 24;
+constexpr int kMaxSeqs = 1 << 16;
+constexpr int kMaxHeads = 512;  // of queries, keys and values together
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+mxgemm_status launched() { return hipGetLastError() == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP; }
+
+// The cache's own rules; pages: whether its keys and values are used
+mxgemm_status check_cache(const mxgemm_kv_cache *c, bool pages, mx::CacheArgs &a)
+{
+    if (!c || !c->offsets || !c->lens || (pages && (!c->k || !c->v || !c->pages)) ||
+        (c->format != MXGEMM_KV_BF16 && c->format != MXGEMM_KV_FP8_E4M3) ||
+        (c->format == MXGEMM_KV_BF16 && (c->k_scale || c->v_scale)))
+        return MXGEMM_ERR_INVALID_ARG;
+    const int D = c->head_dim, P = c->page_size, width = c->format == MXGEMM_KV_BF16 ? 2 : 1;
+    if (c->seqs < 1 || c->seqs > kMaxSeqs || c->kv_heads < 1 || c->kv_heads > kMaxHeads || D < 32 || D > 256 || D % 32 ||
+        P < 16 || P > 65536 || (P & (P - 1)) || c->num_pages < 1 || c->max_pages < 1 || (int64_t)c->max_pages * P > kMaxInt ||
+        c->ld_pages < c->max_pages || c->token_stride < D || c->head_stride < D || c->page_stride < D ||
+        c->token_stride > kMaxInt / 2 / P || c->page_stride > ((int64_t)1 << 40) || c->head_stride > ((int64_t)1 << 40))
+        return MXGEMM_ERR_SHAPE;
+    const int64_t unit = 16 / width;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->token_stride % unit || c->head_stride % unit || c->page_stride % unit ||
+        !aligned(c->pages, 4) || !aligned(c->offsets, 4) || !aligned(c->lens, 4) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return MXGEMM_ERR_ALIGN;
+    a.k = (uint8_t *)c->k;
+    a.v = (uint8_t *)c->v;
+    a.page_b = c->page_stride * width;
+    a.head_b = c->head_stride * width;
+    a.token_b = c->token_stride * width;
+    a.pages = c->pages;
+    a.ld_pages = c->ld_pages;
+    a.offsets = c->offsets;
+    a.lens = c->lens;
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.num_pages = c->num_pages;
+    a.page_shift = __builtin_ctz((unsigned)P);
+    a.seqs = c->seqs;
+    a.max_pages = c->max_pages;
+    a.kv_heads = c->kv_heads;
+    a.D = D;
+    return MXGEMM_OK;
+}
+
+// Tiles of `tile` rows over all sequences and key heads, at most
+int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
+{
+    return kv_heads * (T * group / tile + std::min<int64_t>(T, seqs));
+}
+
+bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
+{
+    return T >= 1 && T <= kMaxTokens && seqs >= 1 && seqs <= kMaxSeqs && kv_heads >= 1 && heads >= kv_heads &&
+           heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && D >= 32 && D <= 256 && D % 32 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxgemm_status mxgemm_rope_frequencies(double *freq, int rot_dim, double base, double factor, double original, double low,
+                                      double high)
+{
+    if (!freq || !(base > 0.0) || !(factor > 0.0) || !std::isfinite(base) || !std::isfinite(factor))
+        return MXGEMM_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim % 2 || rot_dim > 256)
+        return MXGEMM_ERR_SHAPE;
+    const bool parts = low != 0.0 || high != 0.0;
+    if (parts && (!(original > 0.0) || !(low >= 0.0) || !(high > low) || !std::isfinite(original) || !std::isfinite(high)))
+        return MXGEMM_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        const double turns = original * f / 6.283185307179586476925;  // over the original context
+        const double keep = parts ? std::min(1.0, std::max(0.0, (turns - low) / (high - low))) : 0.0;
+        freq[i] = f * (keep + (1.0 - keep) / factor);
+    }
+    return MXGEMM_OK;
+}
+
+mxgemm_status mxgemm_kv_append(const mxgemm_kv_cache *cache, const mxgemm_append *p, int T, hipStream_t stream)
+{
+    if (!p || (!p->Q && !p->K) || (p->Q == nullptr) != (p->Q_out == nullptr) || (p->K == nullptr) != (p->V == nullptr) ||
+        (p->interleaved != 0 && p->interleaved != 1) || (p->rot_dim > 0 && !p->freq))
+        return MXGEMM_ERR_INVALID_ARG;
+    mx::AppendArgs a = {};
+    mxgemm_status st = check_cache(cache, p->K != nullptr, a.c);
+    if (st != MXGEMM_OK)
+        return st;
+    const int D = cache->head_dim, Hk = cache->kv_heads, H = p->Q ? p->heads : 0;
+    if (T < 1 || T > kMaxTokens || (p->Q && H < 1) || H > kMaxHeads || H + 2 * Hk > kMaxHeads || p->rot_dim < 0 || p->rot_dim > D || p->rot_dim % 16 ||
+        (p->Q && (p->ldq < (int64_t)H * D || p->ldqo < (int64_t)H * D)) ||
+        (p->K && (p->ldk < (int64_t)Hk * D || p->ldv < (int64_t)Hk * D)))
+        return MXGEMM_ERR_SHAPE;
+    if (!aligned(p->Q, 16) || !aligned(p->Q_out, 16) || !aligned(p->K, 16) || !aligned(p->V, 16) ||
+        (p->Q && (p->ldq % 8 || p->ldqo % 8)) || (p->K && (p->ldk % 8 || p->ldv % 8)) || !aligned(p->positions, 4) ||
+        !aligned(p->freq, 8))
+        return MXGEMM_ERR_ALIGN;
+    int cu = 0;
+    st = mx::check_device(&cu);
+    if (st != MXGEMM_OK)
+        return st;
+    a.Q = (const uint16_t *)p->Q;
+    a.K = (const uint16_t *)p->K;
+    a.V = (const uint16_t *)p->V;
+    a.QO = (uint16_t *)p->Q_out;
+    a.ldq = p->ldq;
+    a.ldk = p->ldk;
+    a.ldv = p->ldv;
+    a.ldqo = p->ldqo;
+    a.positions = p->positions;
+    a.freq = p->freq;
+    a.factor = p->factor;
+    a.T = T;
+    a.heads = H;
+    a.rot = p->rot_dim;
+    a.interleaved = p->interleaved;
+    a.fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
+    mx::launch_append(a, cu, stream);
+    return launched();
+}
+
+size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv_heads, int head_dim)
+{
+    if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
+        return 0;
+    return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * mx::attn_partial_floats(head_dim) * 4);
+}
+
+mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_attention *p, int T, void *workspace,
+                                     size_t workspace_bytes, hipStream_t stream)
+{
+    if (!p || !p->Q || (!p->O && !p->A) || (p->A == nullptr) != (p->scaleA == nullptr) || (p->causal != 0 && p->causal != 1) ||
+        !std::isfinite(p->scale))
+        return MXGEMM_ERR_INVALID_ARG;
+    const int bits = p->a_format == MXGEMM_FMT_FP4 ? 4 : p->a_format == MXGEMM_FMT_FP8_E4M3 ? 8 : 0;
+    if (!bits)
+        return MXGEMM_ERR_INVALID_ARG;
+    mx::AttnArgs a = {};
+    mxgemm_status st = check_cache(cache, true, a.c);
+    if (st != MXGEMM_OK)
+        return st;
+    const int D = cache->head_dim, Hk = cache->kv_heads, H = p->heads;
+    if (!attention_shape(T, cache->seqs, H, Hk, D) || p->window < 0 || p->max_new < 0 || p->ldq < (int64_t)H * D ||
+        (p->O && p->ldo < (int64_t)H * D) || (p->A && (p->lda < (int64_t)H * D || p->ldsa < H * D / 32)))
+        return MXGEMM_ERR_SHAPE;
+    if (!aligned(p->Q, 16) || p->ldq % 8 || !aligned(p->O, 16) || (p->O && p->ldo % 8) || !aligned(p->lse, 4) ||
+        !aligned(p->sinks, 4) || !aligned(p->A, 16) || (p->A && p->lda % (128 / bits)))
+        return MXGEMM_ERR_ALIGN;
+    const int G = H / Hk;
+    const int64_t units = most_units(T, cache->seqs, G, Hk, mx::kAttnTile);
+    const int64_t groups = cdiv((int64_t)cache->max_pages * cache->page_size, mx::kAttnGroup);
+    if (units > kMaxInt / groups)
+        return MXGEMM_ERR_SHAPE;
+    const size_t need = mxgemm_paged_attention_workspace_bytes(T, cache->seqs, H, Hk, D);
+    if (!workspace || workspace_bytes < need)
+        return MXGEMM_ERR_WORKSPACE;
+    if (!aligned(workspace, 16))
+        return MXGEMM_ERR_ALIGN;
+    int cu = 0;
+    st = mx::check_device(&cu);
+    if (st != MXGEMM_OK)
+        return st;
+    a.Q = (const uint16_t *)p->Q;
+    a.O = (uint16_t *)p->O;
+    a.lse = p->lse;
+    a.A = (uint8_t *)p->A;
+    a.S = (uint8_t *)p->scaleA;
+    a.sinks = p->sinks;
+    a.ldq = p->ldq;
+    a.ldo = p->ldo;
+    a.lda_b = bits == 4 ? p->lda / 2 : p->lda;
+    a.lds = p->ldsa;
+    a.scale = p->scale;
+    a.T = T;
+    a.heads = H;
+    a.group = G;
+    a.causal = p->causal;
+    a.window = p->window;
+    a.a_fp8 = bits == 8;
+    a.counters = (int *)workspace;
+    a.partials = (float *)((uint8_t *)workspace + mx::kAttnCounterBytes);
+    const bool fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
+    const int64_t grid = std::min<int64_t>({units * groups, (int64_t)cu * mx::attn_keys_per_cu(D, fp8), mx::kAttnPieces});
+    mx::launch_attn_keys(a, fp8, (int)grid, stream);
+    return launched();
+}
+
+}  // extern "C"

@@ -574,6 +574,174 @@ typedef struct mxgemm_norm {
  */
 mxgemm_status mxgemm_norm_quantize(const mxgemm_norm *n, int T, int K, hipStream_t stream);
 
+/* ---- attention over a paged cache ---------------------------------------------- */
+
+/*
+ * What stands between a layer's QKV product and its output product when a
+ * model is served, in two operators that hand their device buffers on without
+ * a host copy:
+ *
+ *   mxgemm_run              activations -> queries, keys and values (bf16)
+ *   mxgemm_kv_append        queries and keys turned to their positions; keys
+ *                           and values into the cache's pages
+ *   mxgemm_paged_attention  attention of the new tokens over the pages -> bf16
+ *                           rows and / or the output product's quantized A
+ *   mxgemm_run              the output product
+ *
+ * Forward only, like the rest of the library.  Neither allocates, reads back
+ * or keeps anything: both can be captured into a graph, and calls that share
+ * no output, cache or workspace can overlap.
+ */
+#define MXGEMM_KV_BF16     0
+#define MXGEMM_KV_FP8_E4M3 1
+
+/*
+ * A paged cache and the batch of sequences that uses it.
+ *
+ * Token i of sequence s is row i % page_size of page pages[s][i / page_size];
+ * key head h of that row stands at
+ *
+ *     k + page * page_stride + h * head_stride + row * token_stride
+ *
+ * (strides in elements of the format), v likewise.  Elements are bf16, or E4M3
+ * codes worth code * k_scale[h] (v_scale[h]); NULL scales are 1.
+ *
+ * The batch's new tokens are rows of its activations: those of sequence s are
+ * rows offsets[s] .. offsets[s + 1] - 1 (none: the sequence is left out).
+ * lens[s] counts the tokens of s with the new ones, so that a new token's
+ * position is lens[s] - (offsets[s + 1] - row).
+ *
+ * offsets, lens and pages are device arrays of int32.  offsets have to ascend;
+ * whatever the three hold, no address outside the buffers is formed: offsets
+ * are clamped to [0, T], lens to [0, max_pages * page_size], nothing is written
+ * to a page outside [0, num_pages) and it reads as zeros.  Rows of outputs that
+ * no sequence has are left as they were.
+ *
+ * Limits: head_dim a multiple of 32 up to 256; page_size a power of two from 16
+ * to 65536; seqs <= 65536; max_pages * page_size < 2^31; token_stride *
+ * page_size < 2^30; query, key and value heads together at most 512 (else
+ * MXGEMM_ERR_SHAPE).  k and v 16-byte aligned, strides whole 16 bytes, arrays
+ * 4-byte aligned (else MXGEMM_ERR_ALIGN).
+ */
+typedef struct mxgemm_kv_cache {
+    void *k, *v;
+    int64_t page_stride, head_stride, token_stride; /* elements, of both k and v */
+    const int32_t *pages;   /* [seqs][ld_pages] */
+    int64_t ld_pages;       /* >= max_pages */
+    const int32_t *offsets; /* [seqs + 1] */
+    const int32_t *lens;    /* [seqs] */
+    const float *k_scale;   /* [kv_heads] or NULL (NULL with bf16) */
+    const float *v_scale;
+    int32_t num_pages;      /* pages there are */
+    int32_t page_size;      /* tokens of a page */
+    int32_t seqs;
+    int32_t max_pages;      /* pages of a sequence, at most */
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format;         /* MXGEMM_KV_BF16 or MXGEMM_KV_FP8_E4M3 */
+} mxgemm_kv_cache;
+
+/*
+ * Rotary positions and the append.  Of every head of Q and K the first rot_dim
+ * elements are turned in pairs p = 0 .. rot_dim / 2 - 1 (elements p and p +
+ * rot_dim / 2, or 2p and 2p + 1 with interleaved = 1) by the angle a =
+ * position * freq[p]:
+ *
+ *     x' = factor * (x cos a - y sin a),   y' = factor * (y cos a + x sin a)
+ *
+ * and the others are copied.  Q goes to Q_out; K and V, which is not turned, go
+ * to the new tokens' rows of the cache.  Angles are reduced in 64 bits, the rest
+ * is in fp32 with one rounding to the output's type; an E4M3 code is the fp32
+ * quotient by the head's scale, to nearest even, saturating at 448 (a NaN stays
+ * one).  A token without a place in the cache (a negative position, a page
+ * outside the cache) has its Q turned and nothing written.  Two new tokens must
+ * not have the same place.
+ */
+typedef struct mxgemm_append {
+    const void *Q;            /* bf16 [T][ldq], head h from column h * head_dim; NULL: no queries */
+    void *Q_out;              /* bf16 [T][ldqo]; may be Q (ldqo == ldq); NULL with Q */
+    const void *K, *V;        /* bf16 [T][ldk], [T][ldv]; both NULL: only Q is turned (k, v, pages unused) */
+    int64_t ldq, ldqo, ldk, ldv;
+    const int32_t *positions; /* [T] positions to turn by, or NULL: the tokens' places in the cache */
+    const double *freq;       /* device, [rot_dim / 2], radians a position (mxgemm_rope_frequencies) */
+    float factor;             /* of the turned elements; 1 unless a long context's scaling has one */
+    int32_t heads;            /* query heads */
+    int32_t rot_dim;          /* a multiple of 16 up to head_dim; 0: nothing is turned */
+    int32_t interleaved;
+} mxgemm_append;
+
+/*
+ * 1 <= T <= 2^24.  bf16 pointers 16-byte aligned, their strides multiples of 8
+ * and at least heads * head_dim (kv_heads * head_dim).  Q, K and V may be
+ * columns of one matrix.  Apart from Q_out no output overlaps an input.  Errors:
+ * MXGEMM_ERR_INVALID_ARG (NULL or half a pair, a flag that is not 0 or 1,
+ * another format, scales with bf16), MXGEMM_ERR_SHAPE, MXGEMM_ERR_ALIGN, all
+ * before any HIP call.  Asynchronous on `stream`.
+ */
+mxgemm_status mxgemm_kv_append(const mxgemm_kv_cache *cache, const mxgemm_append *p, int T, hipStream_t stream);
+
+/*
+ * Frequencies for mxgemm_kv_append, computed on the host into host memory:
+ * freq[p] = base^(-2 p / rot_dim), scaled for contexts `factor` times as long as
+ * the `original` one the model was trained on: with low = high = 0 all divided
+ * by factor (1: as they are); else a pair that turns at least `high` times over
+ * the original context keeps its frequency, one that turns at most `low` times
+ * has it divided by factor, and between them the kept share grows linearly with
+ * the turns.  rot_dim even, 2 .. 256; base, factor > 0; 0 <= low < high and
+ * original > 0 where they are used.  No HIP call is made.
+ */
+mxgemm_status mxgemm_rope_frequencies(double *freq, int rot_dim, double base, double factor, double original, double low,
+                                      double high);
+
+/*
+ * Attention of the new tokens over the cache, which holds their own keys and
+ * values already.  Query head h uses key head h / (heads / kv_heads).  A token
+ * at position p sees the keys j < lens[s] with j <= p (causal = 1) and j > p -
+ * window (window > 0), none if p < 0:
+ *
+ *     O[t][h] = sum_j e^(x_j) v_j / (sum_j e^(x_j) + e^sinks[h]),  x_j = scale * q . k_j
+ *     lse[t][h] = log(sum_j e^(x_j) + e^sinks[h])
+ *
+ * (without sinks the last terms are absent; a row without a key is 0, its lse
+ * -inf or the sink).  Keys that a row does not see do not reach it, whatever
+ * they or their values hold.  O is rounded once to bf16; A with scaleA are
+ * those bf16 values quantized (mxgemm_quantize's rule, or MXFP8 as in "mixture
+ * of experts"), blocks of 32 columns of a row.  Products are of bf16 (E4M3 codes
+ * as they are), sums in fp32; e^x is rounded to bf16 for the product with v.
+ */
+typedef struct mxgemm_attention {
+    const void *Q;      /* bf16 [T][ldq], head h from column h * head_dim */
+    void *O;            /* bf16 [T][ldo] or NULL; may be Q (ldo == ldq) */
+    float *lse;         /* [T][heads], dense, or NULL */
+    const float *sinks; /* [heads] or NULL */
+    void *A;            /* [T][lda] codes or NULL (O or A) */
+    void *scaleA;       /* [T][ldsa] scale bytes; NULL with A */
+    int64_t ldq, ldo, lda, ldsa;
+    float scale;        /* finite */
+    int32_t heads;      /* a multiple of kv_heads */
+    int32_t causal;
+    int32_t window;     /* 0: none */
+    int32_t max_new;    /* the most new tokens of a sequence, which chooses the kernel; 0: not known (any value gives the same results but for the order of sums) */
+    int32_t a_format;   /* MXGEMM_FMT_FP4 or MXGEMM_FMT_FP8_E4M3 */
+} mxgemm_attention;
+
+/*
+ * workspace: mxgemm_paged_attention_workspace_bytes(...) device bytes or more,
+ * 16-byte aligned, ZEROED once before its first use and not shared by calls that
+ * can overlap.  Its first 4 KiB are counters, which every call leaves zero
+ * again; the rest needs no clearing, so that calls of any sizes can use one
+ * workspace in turn.  Deterministic: the same call gives the same bits.
+ * bf16 pointers 16-byte aligned, their strides multiples of 8; A as in
+ * mxgemm_quantize.  But for O no output overlaps an input or another output.  Errors:
+ * MXGEMM_ERR_INVALID_ARG, MXGEMM_ERR_SHAPE, MXGEMM_ERR_ALIGN,
+ * MXGEMM_ERR_WORKSPACE, all before any HIP call.  Asynchronous on `stream`.
+ */
+mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_attention *p, int T, void *workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of mxgemm_paged_attention's workspace (0: an invalid shape). */
+size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv_heads, int head_dim);
+
 /* ---- plan / query ------------------------------------------------------------- */
 
 typedef struct mxgemm_info {
