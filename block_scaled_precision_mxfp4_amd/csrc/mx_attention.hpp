@@ -59,5 +59,10 @@ struct AttnArgs {
 int attn_keys_per_cu(int D, bool fp8);
 int64_t attn_partial_floats(int D);
 void launch_attn_keys(const AttnArgs &a, bool fp8, int grid, hipStream_t s);
+// The kernel whose waves hold 32 rows each (mx_attn_rows.hip): rows of its
+// tiles, workgroups per compute unit; whole: no tile is shared.
+int attn_rows_tile(int D);
+int attn_rows_per_cu(int D);
+void launch_attn_rows(const AttnArgs &a, bool fp8, bool whole, int grid, hipStream_t s);
 
 }  // namespace mx

@@ -312,15 +312,17 @@ struct AttnState {
     }
 };
 
-// Scores to P (bf16 pairs, the second product's operands for its two steps of
-// 16 keys), raising the maximum where it has to be.
-template <int ND>
-__device__ __forceinline__ void softmax_block(AttnState<ND> &t, v16f s, float c, v4i (&p)[2])
+// Scores of NB blocks to P (bf16 pairs, the second product's operands for its
+// two steps of 16 keys a block), raising the maximum where it has to be.
+template <int ND, int NB>
+__device__ __forceinline__ void softmax_blocks(AttnState<ND> &t, const v16f (&s)[NB], float c, v4i (&p)[NB][2])
 {
-    float x = fmaxf(s[0], s[1]);
+    float x = s[0][0];
 #pragma unroll
-    for (int g = 2; g < 16; ++g)
-        x = fmaxf(x, s[g]);
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int g = 0; g < 16; ++g)
+            x = fmaxf(x, s[b][g]);
     x = row_max(x) * c;
     if (__builtin_amdgcn_ballot_w64(x > t.m + kRaise)) {
         const float m = fmaxf(t.m, x);
@@ -335,18 +337,21 @@ __device__ __forceinline__ void softmax_block(AttnState<ND> &t, v16f s, float c,
     }
     // a row that has seen no key yet: every score is -inf, p = 0
     const float m = t.m == kNegInf ? 0.0f : t.m;
-    float e[16];
 #pragma unroll
-    for (int g = 0; g < 16; ++g)
-        e[g] = exp2_fast(fmaf(s[g], c, -m));
-    float sum[4];
+    for (int b = 0; b < NB; ++b) {
+        float e[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sum[i] = (e[4 * i] + e[4 * i + 1]) + (e[4 * i + 2] + e[4 * i + 3]);
-    t.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        for (int g = 0; g < 16; ++g)
+            e[g] = exp2_fast(fmaf(s[b][g], c, -m));
+        float sum[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        p[i >> 2][i & 3] = (int)bf16x2_rne(e[2 * i], e[2 * i + 1]);
+        for (int i = 0; i < 4; ++i)
+            sum[i] = (e[4 * i] + e[4 * i + 1]) + (e[4 * i + 2] + e[4 * i + 3]);
+        t.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[b][i >> 2][i & 3] = (int)bf16x2_rne(e[2 * i], e[2 * i + 1]);
+    }
 }
 
 // V^T fragments of columns 32 d .. 32 d + 31, keys' step s (16 keys)
@@ -473,9 +478,11 @@ __device__ __forceinline__ AttnScale attn_scale(const AttnArgs &a, int head)
 
 // A finished row's 8 columns from col on: o relative to 2^m, l the sum; the
 // sink's share joins the sum.  Every lane of a quad has the same row.
-template <typename F>
-__device__ __forceinline__ void finish_row(const AttnArgs &a, int kv_head, int token, int head, int col, float m, float l,
-                                           F &&o, bool live)
+struct RowEnd {
+    float f;    // O's factor
+    float lse;
+};
+__device__ __forceinline__ RowEnd end_row(const AttnArgs &a, int kv_head, int head, float m, float l)
 {
     float w = 1.0f;
     if (a.sinks) {
@@ -487,21 +494,64 @@ __device__ __forceinline__ void finish_row(const AttnArgs &a, int kv_head, int t
         }
     }
     const float vs = a.c.v_scale ? a.c.v_scale[kv_head] : 1.0f;
-    const float f = l == 0.0f ? 0.0f : w / l * vs;
-    v4i x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        x[i] = (int)bf16x2_rne(o(2 * i) * f, o(2 * i + 1) * f);
+    return {l == 0.0f ? 0.0f : w / l * vs, l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2};
+}
+__device__ __forceinline__ void store_row(const AttnArgs &a, int token, int head, int col, v4i x, bool live)
+{
     if (live && a.O)
         *reinterpret_cast<v4i *>(a.O + (int64_t)token * a.ldo + head * a.c.D + col) = x;
-    if (live && a.lse && col == 0)
-        a.lse[(int64_t)token * a.heads + head] = l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
     if (a.A) {
         uint8_t *A = a.A + (int64_t)token * a.lda_b, *S = a.S + (int64_t)token * a.lds;
         if (a.a_fp8)
             quantize_store<true>(x, A, S, head * a.c.D + col, live);
         else
             quantize_store<false>(x, A, S, head * a.c.D + col, live);
+    }
+}
+template <typename F>
+__device__ __forceinline__ void finish_row(const AttnArgs &a, int kv_head, int token, int head, int col, float m, float l,
+                                           F &&o, bool live)
+{
+    const RowEnd e = end_row(a, kv_head, head, m, l);
+    v4i x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = (int)bf16x2_rne(o(2 * i) * e.f, o(2 * i + 1) * e.f);
+    if (live && a.lse && col == 0)
+        a.lse[(int64_t)token * a.heads + head] = e.lse;
+    store_row(a, token, head, col, x, live);
+}
+
+// A wave's 32 finished rows from its registers, through `lds` (32 * DP * 2
+// bytes of its own).  r0: the first row's number among the sequence's rows;
+// rows: how many there are (at most 32); m, l of this lane's row, l of all its keys.
+template <int DP>
+__device__ __forceinline__ void finish_tile(const AttnArgs &a, const AttnSeq &q, int kv_head, int r0, int rows, float m,
+                                            float l, const v16f (&o)[DP / 32], uint8_t *lds, int lane)
+{
+    constexpr int CH = DP / 8;  // 16-byte chunks of a row
+    const int row = lane & 31, rr = r0 + min(row, rows - 1);
+    const int token = q.t0 + rr / a.group, head = kv_head * a.group + rr % a.group;
+    const RowEnd e = end_row(a, kv_head, head, m, l);
+    if (a.lse && lane < rows)
+        a.lse[(int64_t)token * a.heads + head] = e.lse;
+    auto swz = [](int r) { return CH >= 16 ? r & 15 : (r >> 1) & 7; };
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 16; g += 4) {
+            const int c = d * 4 + (g >> 2);
+            v2u x;
+            x[0] = bf16x2_rne(o[d][g] * e.f, o[d][g + 1] * e.f);
+            x[1] = bf16x2_rne(o[d][g + 2] * e.f, o[d][g + 3] * e.f);
+            *reinterpret_cast<v2u *>(lds + row * (DP * 2) + ((c ^ swz(row)) * 16) + (lane >> 5) * 8) = x;
+        }
+#pragma unroll
+    for (int i = 0; i < 32 * CH / 64; ++i) {
+        const int r = (i * 64 + lane) / CH, c = lane % CH;
+        const v4i x = *reinterpret_cast<const v4i *>(lds + r * (DP * 2) + ((c ^ swz(r)) * 16));
+        const int r1 = r0 + min(r, rows - 1);
+        store_row(a, q.t0 + r1 / a.group, kv_head * a.group + r1 % a.group, c * 8, x, r < rows && c * 8 < a.c.D);
     }
 }
 

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     const int wg = blockIdx.x;
     AttnPlan plan;
     int chunk;
-    if (!attn_plan(a, kAttnTile, wg, gridDim.x, lane, plan, chunk))
+    if (!attn_plan(a, kAttnTile, 0, wg, gridDim.x, lane, plan, chunk))
         return;
 
     uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
@@ -134,14 +134,14 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                 const uint32_t slot = (uint32_t)((i % ST) * STAGE);
                 const int key0 = (b0 + wave + i * NW) * 32;
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
-                v16f x = scores<DP, FP8>(ka, slot, qf);
+                v16f x[1] = {scores<DP, FP8>(ka, slot, qf)};
                 const bool masked = key0 < all_lo || key0 + 32 > all_hi;
                 if (masked)
-                    mask_scores(x, row_lo - key0, row_hi - key0, lane);
-                v4i p[2];
-                softmax_block(t, x, sc.c, p);
+                    mask_scores(x[0], row_lo - key0, row_hi - key0, lane);
+                v4i p[1][2];
+                softmax_blocks(t, x, sc.c, p);
                 attn_wait_vm<(ST - 1) * 2 * NI>();
-                values<DP, FP8>(va, slot, p, t, masked, row_lo - key0, row_hi - key0, lane);
+                values<DP, FP8>(va, slot, p[0], t, masked, row_lo - key0, row_hi - key0, lane);
             }
         }
         // merge the waves: O to the wave's ring, rows of DP floats whose
@@ -248,7 +248,7 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 }  // namespace
 
-int64_t attn_partial_floats(int D) { return 32 * ((int64_t)padded(D) + 2); }
+int64_t attn_partial_floats(int D) { return 32 * ((int64_t)padded(D) + 4); }  // (rows: an m and l per lane)
 
 int attn_keys_per_cu(int D, bool fp8)
 {

@@ -5,7 +5,9 @@
 // 128-key groups of its sequence, and all units' groups, in order (sequence,
 // row tile, key head), are one line that is cut into equal pieces, one per
 // workgroup.  A unit that a cut goes through is done by several workgroups:
-// each leaves a partial result, and the last one to arrive adds them up.
+// each leaves a partial result, and the last one to arrive adds them up.  With
+// `whole` every unit counts 1, and with as many workgroups as there can be units
+// none is cut.
 #pragma once
 
 #include "mx_attn.hpp"
@@ -20,17 +22,17 @@ struct AttnPlan {
 };
 
 // Groups of a sequence as a lane sees it
-__device__ __forceinline__ void plan_costs(const AttnArgs &a, const AttnSeq &q, int tile, int &groups)
+__device__ __forceinline__ void plan_costs(const AttnArgs &a, const AttnSeq &q, int tile, int whole, int &groups)
 {
     const int units = seq_tiles(q, a.group, tile) * a.c.kv_heads;
-    groups = units > 0 ? units * seq_groups(q, a.group, tile, a.window) : 0;
+    groups = units > 0 ? units * (whole ? 1 : seq_groups(q, a.group, tile, a.window)) : 0;
 }
 
 // By one wave, the same result in every lane: the line's length and the
 // sequence that piece number `piece` of `pieces` starts in.  False: there is
 // nothing (the piece is past the end, or the offsets count more than T tokens,
 // as those that do not ascend may).
-__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int piece, int pieces, int lane, AttnPlan &p,
+__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int whole, int piece, int pieces, int lane, AttnPlan &p,
                                           int &chunk)
 {
     const int S = a.c.seqs;
@@ -41,7 +43,7 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int piece
         if (s < S) {
             const AttnSeq q = seq_from(a.c, a.T, a.c.offsets[s], a.c.offsets[s + 1], a.c.lens[s]);
             int g;
-            plan_costs(a, q, tile, g);
+            plan_costs(a, q, tile, whole, g);
             groups += g;
             tokens = min(tokens + q.n, a.T + 1);
         }
@@ -64,7 +66,7 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int piece
         int g = 0;
         if (s < min((l + 1) * per, S)) {
             const AttnSeq q = seq_from(a.c, a.T, a.c.offsets[s], a.c.offsets[s + 1], a.c.lens[s]);
-            plan_costs(a, q, tile, g);
+            plan_costs(a, q, tile, whole, g);
         }
         const int g2 = p.start + wave_scan(g);
         const uint64_t past = __builtin_amdgcn_ballot_w64(at < g2);

@@ -17,6 +17,7 @@ constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxSeqs = 1 << 16;
 constexpr int kMaxHeads = 512;  // of queries, keys and values together
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int kKeysRows = 32;   // rows of a sequence and key head up to which its waves share a tile
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -140,7 +141,8 @@ size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv
 {
     if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
         return 0;
-    return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * mx::attn_partial_floats(head_dim) * 4);
+    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::attn_rows_tile(head_dim) / 32 : 1;
+    return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * parts * mx::attn_partial_floats(head_dim) * 4);
 }
 
 mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_attention *p, int T, void *workspace,
@@ -197,6 +199,15 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     a.counters = (int *)workspace;
     a.partials = (float *)((uint8_t *)workspace + mx::kAttnCounterBytes);
     const bool fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
+    const int tile = mx::attn_rows_tile(D);
+    const int most_new = p->max_new > 0 ? std::min(p->max_new, T) : T;
+    if ((int64_t)most_new * G > kKeysRows) {
+        const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
+        const bool whole = tiles >= 2 * (int64_t)cu;
+        const int64_t grid = whole ? tiles : std::min<int64_t>({tiles * groups, (int64_t)cu * mx::attn_rows_per_cu(D), mx::kAttnPieces});
+        mx::launch_attn_rows(a, fp8, whole, (int)grid, stream);
+        return launched();
+    }
     const int64_t grid = std::min<int64_t>({units * groups, (int64_t)cu * mx::attn_keys_per_cu(D, fp8), mx::kAttnPieces});
     mx::launch_attn_keys(a, fp8, (int)grid, stream);
     return launched();
