@@ -40,6 +40,7 @@ constexpr int kAttnTile = 32;    // rows (token, head of a group) that a wave ho
 constexpr int kAttnGroup = 128;  // keys that work is handed out by
 constexpr int kAttnPieces = 512; // workgroups that may leave partial results, at most
 constexpr int kAttnCounterBytes = 4096;
+constexpr int kPlanWhole = 0, kPlanLine = 1, kPlanParts = 2;  // mx_attn_plan.hpp
 struct AttnArgs {
     CacheArgs c;
     const uint16_t *Q;
@@ -58,11 +59,11 @@ struct AttnArgs {
 // per compute unit, and the floats of a partial result.
 int attn_keys_per_cu(int D, bool fp8);
 int64_t attn_partial_floats(int D);
-void launch_attn_keys(const AttnArgs &a, bool fp8, int grid, hipStream_t s);
+void launch_attn_keys(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);
 // The kernel whose waves hold 32 rows each (mx_attn_rows.hip): rows of its
-// tiles, workgroups per compute unit; whole: no tile is shared.
+// tiles, workgroups per compute unit.
 int attn_rows_tile(int D);
 int attn_rows_per_cu(int D);
-void launch_attn_rows(const AttnArgs &a, bool fp8, bool whole, int grid, hipStream_t s);
+void launch_attn_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);
 
 }  // namespace mx

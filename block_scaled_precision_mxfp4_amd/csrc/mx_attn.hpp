@@ -248,11 +248,10 @@ __device__ __forceinline__ int attn_page(const CacheArgs &c, const int32_t *tabl
 
 // ---- products and softmax
 
-// This lane's Q fragments (its row's columns), negated where the scores' scale
-// is negative; zeros for rows and columns that do not exist.
+// This lane's Q fragments (its row's columns); zeros for rows and columns that
+// do not exist.
 template <int DP, bool FP8>
-__device__ __forceinline__ void load_q(const AttnArgs &a, const uint16_t *row, bool live, bool negate, int lane,
-                                       v4i (&q)[DP / 16])
+__device__ __forceinline__ void load_q(const AttnArgs &a, const uint16_t *row, bool live, int lane, v4i (&q)[DP / 16])
 {
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
@@ -260,11 +259,18 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const uint16_t *row, b
         q[s] = v4i{0, 0, 0, 0};
         if (live && col < a.c.D)
             q[s] = *reinterpret_cast<const v4i *>(row + col);
-        if (negate)
+    }
+}
+// Negated, where the scores' scale is negative
+template <int NS>
+__device__ __forceinline__ void negate_q(v4i (&q)[NS], bool negate)
+{
+    if (negate)
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 q[s][i] ^= (int)0x80008000;
-    }
 }
 
 // S^T of one block of 32 keys in LDS

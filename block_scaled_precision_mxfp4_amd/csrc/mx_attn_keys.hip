@@ -26,13 +26,12 @@ struct KeysShape {
 };
 
 template <int DP, bool FP8>
-__global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_kernel(AttnArgs a)
+__global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_kernel(AttnArgs a, int mode)
 {
     using L = AttnLds<DP, FP8>;
     using SH = KeysShape<DP, FP8>;
     constexpr int NW = SH::NW, ST = SH::ST, STAGE = SH::STAGE;
     constexpr int NI = 2 * L::NIH;        // load instructions of a block of K, or of V
-    constexpr int GB = kAttnGroup / 32;   // blocks of a group
     constexpr int QC = DP / 8;            // 8-column pieces of a row
     __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
     __shared__ float s_ml[NW][32][2];
@@ -42,8 +41,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
     AttnPlan plan;
-    int chunk;
-    if (!attn_plan(a, kAttnTile, 0, wg, gridDim.x, lane, plan, chunk))
+    if (!attn_plan(a, kAttnTile, mode, wg, gridDim.x, lane, plan))
         return;
 
     uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
@@ -52,31 +50,29 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     L::k_addr(lds_addr(mine), lane, ka);
     L::v_addr(lds_addr(mine) + L::BLOCK, lane, va);
 
-    int at = wg * chunk;
-    const int end = min(at + chunk, plan.total);
+    int at = wg * plan.chunk;
+    const int end = min(at + plan.chunk, plan.total);
     int s = plan.s, seq_start = plan.start;
-    AttnSeq q = load_seq(a.c, a.T, s);
-    int cost = seq_groups(q, a.group, kAttnTile, a.window);
-    int units = seq_tiles(q, a.group, kAttnTile) * a.c.kv_heads;
+    AttnSeq q = plan.q;
+    int cost = seq_steps(a, q, kAttnTile, plan.per), units = seq_units(a, q, kAttnTile);
     while (at < end) {
-        while (at >= seq_start + units * cost) {  // (the line's end is a sequence's: this stops before the last one)
+        while (at >= seq_start + units * cost) {
             seq_start += units * cost;
             if (++s >= a.c.seqs)
                 return;
             q = load_seq(a.c, a.T, s);
-            cost = seq_groups(q, a.group, kAttnTile, a.window);
-            units = seq_tiles(q, a.group, kAttnTile) * a.c.kv_heads;
+            cost = seq_steps(a, q, kAttnTile, plan.per);
+            units = seq_units(a, q, kAttnTile);
         }
-        const int u = (at - seq_start) / cost;
-        const int unit_start = seq_start + u * cost;
+        const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
         const int tile = u / a.c.kv_heads, head = u % a.c.kv_heads;
         const int piece_end = min(end, unit_start + cost);
         // its rows, and the keys that they see
         const int r0 = tile * kAttnTile, rows = min(q.n * a.group - r0, kAttnTile);
         int lo, hi;
         tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
-        const int g0 = lo / kAttnGroup;
-        const int b0 = max((g0 + at - unit_start) * GB, lo / 32), b1 = min((g0 + piece_end - unit_start) * GB, (hi + 31) / 32);
+        const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
+        const int b0 = max(keys.lo, lo) / 32, b1 = (keys.hi + 31) / 32;
         const int nb = max((b1 - b0 - wave + NW - 1) / NW, 0);  // this wave's blocks: b0 + wave, + NW, ...
 
         const int32_t *table = a.c.pages + (int64_t)s * a.c.ld_pages;
@@ -112,25 +108,26 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
         const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
         if (nb > 0) {
-            int pg0, pg1;
+            int pg0[ST], pg1[ST];
 #pragma unroll
-            for (int i = 0; i < ST - 1; ++i) {
-                pages(i, pg0, pg1);
-                issue(i, pg0, pg1);
-            }
-            pages(ST - 1, pg0, pg1);
+            for (int i = 0; i < ST; ++i)
+                pages(i, pg0[i], pg1[i]);
             v4i qf[L::NS];
             {
                 const int hq = head * a.group + (r0 + row) % a.group;
-                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + hq * a.c.D, row < rows && !sc.zero, sc.negate, lane,
-                                qf);
+                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + hq * a.c.D, row < rows && !sc.zero, lane, qf);
             }
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i)
+                issue(i, pg0[i], pg1[i]);
+            int next0 = pg0[ST - 1], next1 = pg1[ST - 1];
+            negate_q(qf, sc.negate);
             // keys that every row of the tile sees
             const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 31) : 0;
             const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
             for (int i = 0; i < nb; ++i) {
-                issue(i + ST - 1, pg0, pg1);
-                pages(i + ST, pg0, pg1);
+                issue(i + ST - 1, next0, next1);
+                pages(i + ST, next0, next1);
                 const uint32_t slot = (uint32_t)((i % ST) * STAGE);
                 const int key0 = (b0 + wave + i * NW) * 32;
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
@@ -166,82 +163,108 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         // the unit's workgroups (at most one unit that goes on behind a workgroup
         // starts in it: its counter is that workgroup's), and this one's place for
         // a partial result
-        const int first = unit_start / chunk, last = (unit_start + cost - 1) / chunk;
-        const bool whole = first == last;
-        const int64_t floats = 32 * (DP + 2);
-        float *part = a.partials + (2 * (int64_t)wg + (unit_start > wg * chunk ? 1 : 0)) * floats;
-        for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
-            const int r = it / QC, c8 = it % QC;
-            const bool live = r < rows && c8 * 8 < a.c.D;
-            const int rr = min(r, rows - 1);
-            float m = kNegInf, l = 0.0f, o[8] = {};
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                m = fmaxf(m, s_ml[w][rr][0]);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float f = m == kNegInf ? 1.0f : exp2_fast(s_ml[w][rr][0] - m);
-                l += f * s_ml[w][rr][1];
-                const float *src = reinterpret_cast<const float *>(ring + w * (ST * STAGE)) + rr * DP;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const v4f x = *reinterpret_cast<const v4f *>(src + (((2 * c8 + h) ^ (rr & 15)) * 4));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[4 * h + e] += f * x[e];
-                }
-            }
-            if (whole) {
-                const int i = (r0 + rr) / a.group;
-                finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
-            } else if (live) {
-                const __amdgpu_buffer_rsrc_t to = make_rsrc_u(part, (uint32_t)(floats * 4));
-                store16_coherent(to, (uint32_t)((r * DP + c8 * 8) * 4), v4f{o[0], o[1], o[2], o[3]});
-                store16_coherent(to, (uint32_t)((r * DP + c8 * 8 + 4) * 4), v4f{o[4], o[5], o[6], o[7]});
-                if (c8 == 0)
-                    __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(m), __float_as_uint(l)}, to,
-                                                          (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
-            }
-        }
-        if (!whole && split_arrive_last_via(a.counters + first, last - first + 1, &s_last)) {
-            // the first workgroup's part of this unit is its last, unless the
-            // unit starts with it; the others' is their first
-            const __amdgpu_buffer_rsrc_t all = make_rsrc_u(a.partials + 2 * (int64_t)first * floats,
-                                                           (uint32_t)((last - first + 1) * 2 * floats * 4));
-            const int off = unit_start > first * chunk ? 1 : 0;
+        const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
+        constexpr int FLOATS = 32 * (DP + 2);
+        const __amdgpu_buffer_rsrc_t part = make_rsrc_u(
+            a.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * FLOATS, FLOATS * 4);
+        // what the waves have in LDS, added up: the result, or this workgroup's part of it
+        auto merge = [&](bool result) __attribute__((always_inline)) {
             for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
                 const int r = it / QC, c8 = it % QC;
                 const bool live = r < rows && c8 * 8 < a.c.D;
                 const int rr = min(r, rows - 1);
                 float m = kNegInf, l = 0.0f, o[8] = {};
-                for (int w = 0; w <= last - first; ++w) {
-                    const uint32_t base = (uint32_t)((2 * w + (w == 0 ? off : 0)) * floats * 4);
-                    const v2u ml = __builtin_amdgcn_raw_buffer_load_b64(all, base + (32 * DP + 2 * rr) * 4, 0, kCoherent);
-                    const v4f x0 = load16_coherent(all, base + (uint32_t)((rr * DP + c8 * 8) * 4));
-                    const v4f x1 = load16_coherent(all, base + (uint32_t)((rr * DP + c8 * 8 + 4) * 4));
-                    const float mw = __uint_as_float(ml[0]), n = fmaxf(m, mw);
-                    const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
-                    m = n;
-                    l = l * f0 + __uint_as_float(ml[1]) * f1;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = o[e] * f0 + x0[e] * f1;
-                        o[4 + e] = o[4 + e] * f0 + x1[e] * f1;
+                for (int w = 0; w < NW; ++w)
+                    m = fmaxf(m, s_ml[w][rr][0]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const float f = m == kNegInf ? 1.0f : exp2_fast(s_ml[w][rr][0] - m);
+                    l += f * s_ml[w][rr][1];
+                    const float *src = reinterpret_cast<const float *>(ring + w * (ST * STAGE)) + rr * DP;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const v4f x = *reinterpret_cast<const v4f *>(src + (((2 * c8 + h) ^ (rr & 15)) * 4));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[4 * h + e] += f * x[e];
                     }
                 }
-                const int i = (r0 + rr) / a.group;
-                finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
+                if (result) {
+                    const int i = (r0 + rr) / a.group;
+                    finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
+                } else if (live) {
+                    store16_coherent(part, (uint32_t)((r * DP + c8 * 8) * 4), v4f{o[0], o[1], o[2], o[3]});
+                    store16_coherent(part, (uint32_t)((r * DP + c8 * 8 + 4) * 4), v4f{o[4], o[5], o[6], o[7]});
+                    if (c8 == 0)
+                        __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(m), __float_as_uint(l)}, part,
+                                                              (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
+                }
+            }
+        };
+        bool done = first == last;
+        if (!done) {
+            merge(false);
+            done = split_arrive_last_via(a.counters + first, last - first + 1, &s_last);
+            if (done) {
+                // each wave adds up every NW-th part, PB of them in flight, into
+                // its ring.  The first workgroup's part of this unit is its last
+                // one unless the unit starts with it; the others' is their first
+                constexpr int PB = 8;
+                const __amdgpu_buffer_rsrc_t all =
+                    make_rsrc_u(a.partials + 2 * (int64_t)first * FLOATS, (uint32_t)(last - first + 1) * (2 * FLOATS * 4));
+                const uint32_t off = unit_start > first * plan.chunk ? FLOATS * 4 : 0;
+                const int parts = last - first + 1;
+                for (int it = lane; it < rows * QC; it += 64) {
+                    const int r = it / QC, c8 = it % QC;
+                    float m = kNegInf, l = 0.0f, o[8] = {};
+                    for (int w0 = wave; w0 < parts; w0 += NW * PB) {
+                        v2u ml[PB];
+                        v4f x[PB][2];
+#pragma unroll
+                        for (int i = 0; i < PB; ++i) {
+                            const int w = min(w0 + i * NW, parts - 1);  // (past the end: the last one, not added)
+                            const uint32_t base = (uint32_t)w * (2 * FLOATS * 4) + (w == 0 ? off : 0);
+                            ml[i] = __builtin_amdgcn_raw_buffer_load_b64(all, base + (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
+                            x[i][0] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8) * 4));
+                            x[i][1] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8 + 4) * 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < PB; ++i) {
+                            if (w0 + i * NW >= parts)
+                                break;
+                            const float mw = __uint_as_float(ml[i][0]), n = fmaxf(m, mw);
+                            const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
+                            m = n;
+                            l = l * f0 + __uint_as_float(ml[i][1]) * f1;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = o[e] * f0 + x[i][e >> 2][e & 3] * f1;
+                        }
+                    }
+                    float *dst = reinterpret_cast<float *>(mine) + r * DP;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<v4f *>(dst + (((2 * c8 + h) ^ (r & 15)) * 4)) = v4f{o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
+                    if (c8 == 0) {
+                        s_ml[wave][r][0] = m;
+                        s_ml[wave][r][1] = l;
+                    }
+                }
+                __syncthreads();
             }
         }
+        if (done)
+            merge(true);
         __syncthreads();  // the rings and s_ml are free again
         at = piece_end;
     }
 }
 
 template <int DP, bool FP8>
-void launch(const AttnArgs &a, int grid, hipStream_t s)
+void launch(const AttnArgs &a, int plan, int grid, hipStream_t s)
 {
-    mx_attn_keys_kernel<DP, FP8><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a);
+    mx_attn_keys_kernel<DP, FP8><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a, plan);
 }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -259,12 +282,12 @@ int attn_keys_per_cu(int D, bool fp8)
     }
 }
 
-void launch_attn_keys(const AttnArgs &a, bool fp8, int grid, hipStream_t s)
+void launch_attn_keys(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
 {
     switch (padded(a.c.D)) {
-    case 64: return fp8 ? launch<64, true>(a, grid, s) : launch<64, false>(a, grid, s);
-    case 128: return fp8 ? launch<128, true>(a, grid, s) : launch<128, false>(a, grid, s);
-    default: return fp8 ? launch<256, true>(a, grid, s) : launch<256, false>(a, grid, s);
+    case 64: return fp8 ? launch<64, true>(a, plan, grid, s) : launch<64, false>(a, plan, grid, s);
+    case 128: return fp8 ? launch<128, true>(a, plan, grid, s) : launch<128, false>(a, plan, grid, s);
+    default: return fp8 ? launch<256, true>(a, plan, grid, s) : launch<256, false>(a, plan, grid, s);
     }
 }
 

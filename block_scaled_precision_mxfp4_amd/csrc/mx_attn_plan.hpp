@@ -1,13 +1,18 @@
 // How the attention kernels' work is handed out, found on the device: the host
 // knows the new tokens and sequences but no length.
 //
-// A unit is one tile of a sequence's rows and one key head.  Its cost is the
-// 128-key groups of its sequence, and all units' groups, in order (sequence,
-// row tile, key head), are one line that is cut into equal pieces, one per
-// workgroup.  A unit that a cut goes through is done by several workgroups:
-// each leaves a partial result, and the last one to arrive adds them up.  With
-// `whole` every unit counts 1, and with as many workgroups as there can be units
-// none is cut.
+// A unit is one tile of a sequence's rows and one key head.  Its cost is its
+// sequence's 128-key groups, in steps of `per` groups, and all units' steps, in
+// order (sequence, row tile, key head), are one line that is cut into equal
+// pieces, one per workgroup.  A unit that a cut goes through is done by several
+// workgroups: each leaves a partial result, and the last one to arrive adds
+// them up.
+//   kPlanWhole  a unit is one step, as many workgroups as there can be units
+//   kPlanLine   steps of one group: equal work, but most workgroups do the end
+//               of one unit and the start of another, each with its latency
+//   kPlanParts  few units: steps as long as it takes for every workgroup to
+//               have one step at most (one token over 4096 keys, 8 key heads:
+//               21 us in line, where 4 of 132 workgroups did parts of two units)
 #pragma once
 
 #include "mx_attn.hpp"
@@ -16,68 +21,119 @@
 namespace mx {
 
 struct AttnPlan {
-    int total;      // groups of all units
-    int s;          // sequence that group `at` is in
-    int start;      // first group of the sequence's units
+    int total;   // steps of all units
+    int chunk;   // steps of a workgroup
+    int per;     // groups of a step
+    int s;       // sequence that the workgroup's first step is in
+    int start;   // first step of that sequence's units
+    AttnSeq q;   // that sequence
 };
 
-// Groups of a sequence as a lane sees it
-__device__ __forceinline__ void plan_costs(const AttnArgs &a, const AttnSeq &q, int tile, int whole, int &groups)
+__device__ __forceinline__ int seq_steps(const AttnArgs &a, const AttnSeq &q, int tile, int per)
 {
-    const int units = seq_tiles(q, a.group, tile) * a.c.kv_heads;
-    groups = units > 0 ? units * (whole ? 1 : seq_groups(q, a.group, tile, a.window)) : 0;
+    return (seq_groups(q, a.group, tile, a.window) + per - 1) / per;
+}
+__device__ __forceinline__ int seq_units(const AttnArgs &a, const AttnSeq &q, int tile)
+{
+    return seq_tiles(q, a.group, tile) * a.c.kv_heads;
 }
 
-// By one wave, the same result in every lane: the line's length and the
-// sequence that piece number `piece` of `pieces` starts in.  False: there is
-// nothing (the piece is past the end, or the offsets count more than T tokens,
-// as those that do not ascend may).
-__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int whole, int piece, int pieces, int lane, AttnPlan &p,
-                                          int &chunk)
+__device__ __forceinline__ AttnSeq seq_of_lane(const AttnArgs &a, int s)
+{
+    return seq_from(a.c, a.T, a.c.offsets[s], a.c.offsets[s + 1], a.c.lens[s]);
+}
+__device__ __forceinline__ AttnSeq lane_seq(const AttnSeq &q, int lane)
+{
+    return {__builtin_amdgcn_readlane(q.t0, lane), __builtin_amdgcn_readlane(q.n, lane), __builtin_amdgcn_readlane(q.len, lane)};
+}
+__device__ __forceinline__ int wave_total(int x) { return __builtin_amdgcn_readlane(wave_scan(x), 63); }
+
+// The keys of steps [from, to) of a unit that sees [lo, hi), from a whole group on
+struct KeyRange {
+    int lo, hi;
+};
+__device__ __forceinline__ KeyRange step_keys(int lo, int hi, int from, int to, int per)
+{
+    const int first = lo / kAttnGroup * kAttnGroup;
+    const int64_t k0 = first + (int64_t)from * per * kAttnGroup, k1 = first + (int64_t)to * per * kAttnGroup;
+    return {(int)min(k0, (int64_t)hi), (int)min(k1, (int64_t)hi)};
+}
+
+// By one wave, the same result in every lane: the plan, and where workgroup
+// `wg` of `wgs` starts.  False: it has nothing (or the offsets count more than T
+// tokens, as those that do not ascend may).
+__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int mode, int wg, int wgs, int lane, AttnPlan &p)
 {
     const int S = a.c.seqs;
-    const int per = (S + 63) / 64;  // sequences of a lane, in order
-    int groups = 0, tokens = 0;
-    for (int i = 0; i < per; ++i) {
-        const int s = lane * per + i;
+    const int each = (S + 63) / 64;  // sequences of a lane, in order
+    AttnSeq q = {0, 0, 0};
+    int units = 0, steps = 0, tokens = 0;
+    p.per = mode == kPlanWhole ? 1 << 24 : 1;
+    for (int i = 0; i < each; ++i) {
+        const int s = lane * each + i;
         if (s < S) {
-            const AttnSeq q = seq_from(a.c, a.T, a.c.offsets[s], a.c.offsets[s + 1], a.c.lens[s]);
-            int g;
-            plan_costs(a, q, tile, whole, g);
-            groups += g;
+            q = seq_of_lane(a, s);
+            const int u = seq_units(a, q, tile);
+            units += u;
+            steps += u * seq_steps(a, q, tile, p.per);
             tokens = min(tokens + q.n, a.T + 1);
         }
     }
-    const int g_to = wave_scan(groups);
-    const int all_tokens = __builtin_amdgcn_readlane(wave_scan(tokens), 63);
-    p.total = __builtin_amdgcn_readlane(g_to, 63);
-    chunk = (p.total + pieces - 1) / pieces;
-    const int at = piece * chunk;
-    if (all_tokens > a.T || at >= p.total)
+    if (wave_total(tokens) > a.T)
         return false;
-    const int l = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(at < g_to)) - 1;
-    p.start = __builtin_amdgcn_readlane(g_to - groups, l);
-    p.s = l * per;
-    if (per == 1)
+    int to = wave_scan(steps);
+    p.total = __builtin_amdgcn_readlane(to, 63);
+    p.chunk = (p.total + wgs - 1) / wgs;
+    if (mode == kPlanParts && each == 1 && p.chunk > 0) {
+        // the host takes this with at most half as many units as workgroups,
+        // so that steps of total / (wgs - units) groups are long enough
+        const int groups = units > 0 ? steps / units : 0;
+        const int all = wave_total(units);
+        const int most = (p.total + wgs - all - 1) / max(wgs - all, 1);
+        int per = p.chunk, n = 0;
+        for (int i = 0; i < 4; ++i) {
+            n = wave_total(units * ((groups + per - 1) / per));
+            if (n <= wgs)
+                break;
+            per = min(max(per + 1, per * n / wgs), max(most, 1));
+        }
+        if (n > wgs)
+            per = max(most, 1);
+        p.per = per;
+        steps = units * ((groups + per - 1) / per);
+        to = wave_scan(steps);
+        p.total = __builtin_amdgcn_readlane(to, 63);
+        p.chunk = (p.total + wgs - 1) / wgs;
+    }
+    const int at = wg * p.chunk;
+    if (at >= p.total)
+        return false;
+    const int l = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(at < to)) - 1;
+    p.start = __builtin_amdgcn_readlane(to - steps, l);
+    p.s = l * each;
+    if (each == 1) {
+        p.q = lane_seq(q, l);
         return true;
+    }
     // within that lane's sequences
     for (int s0 = p.s;; s0 += 64) {
         const int s = s0 + lane;
-        int g = 0;
-        if (s < min((l + 1) * per, S)) {
-            const AttnSeq q = seq_from(a.c, a.T, a.c.offsets[s], a.c.offsets[s + 1], a.c.lens[s]);
-            plan_costs(a, q, tile, whole, g);
+        int n = 0;
+        if (s < min((l + 1) * each, S)) {
+            q = seq_of_lane(a, s);
+            n = seq_units(a, q, tile) * seq_steps(a, q, tile, p.per);
         }
-        const int g2 = p.start + wave_scan(g);
-        const uint64_t past = __builtin_amdgcn_ballot_w64(at < g2);
+        const int upto = p.start + wave_scan(n);
+        const uint64_t past = __builtin_amdgcn_ballot_w64(at < upto);
         if (past) {
             const int m = __ffsll((unsigned long long)past) - 1;
             p.s = s0 + m;
-            p.start = __builtin_amdgcn_readlane(g2 - g, m);
+            p.start = __builtin_amdgcn_readlane(upto - n, m);
+            p.q = lane_seq(q, m);
             return true;
         }
-        p.start = __builtin_amdgcn_readlane(g2, 63);
-        if (s0 + 64 >= (l + 1) * per)
+        p.start = __builtin_amdgcn_readlane(upto, 63);
+        if (s0 + 64 >= (l + 1) * each)
             return false;
     }
 }

@@ -18,7 +18,7 @@ struct RowsShape {
 };
 
 template <int DP, bool FP8>
-__global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(AttnArgs a, int whole)
+__global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(AttnArgs a, int mode)
 {
     using L = AttnLds<DP, false>;  // in LDS the elements are bf16
     using SH = RowsShape<DP>;
@@ -35,8 +35,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
     AttnPlan plan;
-    int chunk;
-    if (!attn_plan(a, TM, whole, wg, gridDim.x, lane, plan, chunk))
+    if (!attn_plan(a, TM, mode, wg, gridDim.x, lane, plan))
         return;
 
     // this lane's places in the cache's rows and in a stage
@@ -63,35 +62,29 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
     L::k_addr(lds_addr(ring), lane, ka);
     L::v_addr(lds_addr(ring) + KT * L::ROWB, lane, va);
 
-    int at = wg * chunk;
-    const int end = min(at + chunk, plan.total);
+    int at = wg * plan.chunk;
+    const int end = min(at + plan.chunk, plan.total);
     int s = plan.s, seq_start = plan.start;
-    AttnSeq q = load_seq(a.c, a.T, s);
-    auto cost_of = [&](const AttnSeq &x) { return whole ? 1 : seq_groups(x, a.group, TM, a.window); };
-    int cost = cost_of(q), units = seq_tiles(q, a.group, TM) * a.c.kv_heads;
+    AttnSeq q = plan.q;
+    int cost = seq_steps(a, q, TM, plan.per), units = seq_units(a, q, TM);
     while (at < end) {
         while (at >= seq_start + units * cost) {
             seq_start += units * cost;
             if (++s >= a.c.seqs)
                 return;
             q = load_seq(a.c, a.T, s);
-            cost = cost_of(q);
-            units = seq_tiles(q, a.group, TM) * a.c.kv_heads;
+            cost = seq_steps(a, q, TM, plan.per);
+            units = seq_units(a, q, TM);
         }
-        const int u = (at - seq_start) / cost;
-        const int unit_start = seq_start + u * cost;
+        const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
         // the tiles with the most keys first
         const int tile = units / a.c.kv_heads - 1 - u / a.c.kv_heads, head = u % a.c.kv_heads;
         const int piece_end = min(end, unit_start + cost);
         const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
         int lo, hi;
         tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
-        int k0 = lo / KT * KT, k1 = hi;
-        if (!whole) {
-            const int g0 = lo / kAttnGroup;
-            k0 = max((g0 + at - unit_start) * kAttnGroup, k0);
-            k1 = min((g0 + piece_end - unit_start) * kAttnGroup, hi);
-        }
+        const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
+        const int k0 = max(keys.lo, lo / KT * KT), k1 = keys.hi;
         const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
 
         const int32_t *table = a.c.pages + (int64_t)s * a.c.ld_pages;
@@ -145,7 +138,8 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const int any_hi = wrows > 0 ? __builtin_amdgcn_readlane(row_hi, 31) : 0;
         v4i qf[L::NS];
         load_q<DP, false>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + (head * a.group + rr % a.group) * a.c.D,
-                          row < wrows && !sc.zero, sc.negate, lane, qf);
+                          row < wrows && !sc.zero, lane, qf);
+        negate_q(qf, sc.negate);
         if (nt > 0) {
             constexpr int AHEAD = ST - 1;
             if constexpr (FP8) {
@@ -192,13 +186,13 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         attn_wait_vm<0>();
         t.l = row_sum(t.l);
         __syncthreads();  // the ring is free
-        const int first = unit_start / chunk, last = (unit_start + cost - 1) / chunk;
+        const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
         bool done = first == last;
         if (!done) {
             // a partial result: a wave's registers as they are
             constexpr int64_t PW = 64 * (L::ND * 16 + 2);  // floats of a wave
             const __amdgpu_buffer_rsrc_t to =
-                make_rsrc_u(a.partials + (2 * (int64_t)wg + (unit_start > wg * chunk ? 1 : 0)) * (NW * PW) + wave * PW, PW * 4);
+                make_rsrc_u(a.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * (NW * PW) + wave * PW, PW * 4);
             if (wrows > 0) {
 #pragma unroll
                 for (int d = 0; d < L::ND; ++d)
@@ -211,7 +205,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
             }
             done = split_arrive_last_via(a.counters + first, last - first + 1, &s_last);
             if (done && wrows > 0) {
-                const int off = unit_start > first * chunk ? 1 : 0;
+                const int off = unit_start > first * plan.chunk ? 1 : 0;
                 t.reset();
                 for (int w = 0; w <= last - first; ++w) {
                     const __amdgpu_buffer_rsrc_t from = make_rsrc_u(
@@ -243,12 +237,12 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 template <int DP>
-void launch(const AttnArgs &a, bool fp8, bool whole, int grid, hipStream_t s)
+void launch(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
 {
     if (fp8)
-        mx_attn_rows_kernel<DP, true><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, whole);
+        mx_attn_rows_kernel<DP, true><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
     else
-        mx_attn_rows_kernel<DP, false><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, whole);
+        mx_attn_rows_kernel<DP, false><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
 }
 
 }  // namespace
@@ -256,12 +250,12 @@ void launch(const AttnArgs &a, bool fp8, bool whole, int grid, hipStream_t s)
 int attn_rows_tile(int D) { return padded(D) == 256 ? RowsShape<256>::TM : RowsShape<128>::TM; }
 int attn_rows_per_cu(int) { return 1; }
 
-void launch_attn_rows(const AttnArgs &a, bool fp8, bool whole, int grid, hipStream_t s)
+void launch_attn_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
 {
     switch (padded(a.c.D)) {
-    case 64: return launch<64>(a, fp8, whole, grid, s);
-    case 128: return launch<128>(a, fp8, whole, grid, s);
-    default: return launch<256>(a, fp8, whole, grid, s);
+    case 64: return launch<64>(a, fp8, plan, grid, s);
+    case 128: return launch<128>(a, fp8, plan, grid, s);
+    default: return launch<256>(a, fp8, plan, grid, s);
     }
 }
 

@@ -199,17 +199,18 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     a.counters = (int *)workspace;
     a.partials = (float *)((uint8_t *)workspace + mx::kAttnCounterBytes);
     const bool fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
-    const int tile = mx::attn_rows_tile(D);
     const int most_new = p->max_new > 0 ? std::min(p->max_new, T) : T;
-    if ((int64_t)most_new * G > kKeysRows) {
-        const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
-        const bool whole = tiles >= 2 * (int64_t)cu;
-        const int64_t grid = whole ? tiles : std::min<int64_t>({tiles * groups, (int64_t)cu * mx::attn_rows_per_cu(D), mx::kAttnPieces});
-        mx::launch_attn_rows(a, fp8, whole, (int)grid, stream);
-        return launched();
+    const bool rows = (int64_t)most_new * G > kKeysRows;
+    const int64_t tiles = rows ? most_units(T, cache->seqs, G, Hk, mx::attn_rows_tile(D)) : units;
+    const int64_t wgs = std::min<int64_t>((int64_t)cu * (rows ? mx::attn_rows_per_cu(D) : mx::attn_keys_per_cu(D, fp8)), mx::kAttnPieces);
+    if (rows) {
+        if (tiles >= 2 * wgs)
+            mx::launch_attn_rows(a, fp8, mx::kPlanWhole, (int)tiles, stream);
+        else
+            mx::launch_attn_rows(a, fp8, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
+    } else {
+        mx::launch_attn_keys(a, fp8, 2 * tiles <= wgs ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     }
-    const int64_t grid = std::min<int64_t>({units * groups, (int64_t)cu * mx::attn_keys_per_cu(D, fp8), mx::kAttnPieces});
-    mx::launch_attn_keys(a, fp8, (int)grid, stream);
     return launched();
 }
 
