@@ -55,11 +55,16 @@ struct AttnArgs {
     int *counters;           // [kAttnPieces], zero between calls
     float *partials;
 };
-// The kernel whose waves take keys in turn (mx_attn_keys.hip).  Its workgroups
-// per compute unit, and the floats of a partial result.
-int attn_keys_per_cu(int D, bool fp8);
+// The kernel whose waves take keys in turn (mx_attn_keys.hip): workgroups per
+// compute unit; tiles of 32 and of 64 rows (may be null).
+typedef void (*AttnLaunchFn)(const AttnArgs &, int plan, int grid, hipStream_t);
+struct AttnKeysKernel {
+    int per_cu;
+    AttnLaunchFn launch[2];
+};
+AttnKeysKernel attn_keys_kernel(int D, bool fp8);
+// Floats of 32 rows of a partial result, at most
 int64_t attn_partial_floats(int D);
-void launch_attn_keys(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);
 // The kernel whose waves hold 32 rows each (mx_attn_rows.hip): rows of its
 // tiles, workgroups per compute unit.
 int attn_rows_tile(int D);

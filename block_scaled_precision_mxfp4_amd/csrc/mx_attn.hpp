@@ -273,12 +273,15 @@ __device__ __forceinline__ void negate_q(v4i (&q)[NS], bool negate)
                 q[s][i] ^= (int)0x80008000;
 }
 
-// S^T of one block of 32 keys in LDS
-template <int DP, bool FP8>
-__device__ __forceinline__ v16f scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF], uint32_t at, const v4i (&q)[DP / 16])
+// S^T of one block of 32 keys in LDS, for NT tiles of 32 rows
+template <int DP, bool FP8, int NT>
+__device__ __forceinline__ void scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF], uint32_t at, const v4i (&q)[NT][DP / 16],
+                                       v16f (&s)[NT])
 {
     using L = AttnLds<DP, FP8>;
-    v16f s = {};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        s[n] = v16f{};
     constexpr int B = L::KF < 8 ? L::KF : 8;  // fragments read together
     static_for<L::KF / B>([&](auto bc) {
         v4i f[B];
@@ -290,17 +293,23 @@ __device__ __forceinline__ v16f scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF
             lds_wait_n<B - I - 2>(f[I], f[I + 1]);
 #pragma unroll
             for (int i = I; i < I + 2; ++i) {
-                const int n = bc.value * B + i;
+                const int k = bc.value * B + i;
                 if constexpr (FP8) {
-                    s = mfma32(bf16_of_fp8(v2u{(uint32_t)f[i][0], (uint32_t)f[i][1]}), q[2 * n], s);
-                    s = mfma32(bf16_of_fp8(v2u{(uint32_t)f[i][2], (uint32_t)f[i][3]}), q[2 * n + 1], s);
+                    const v4i lo = bf16_of_fp8(v2u{(uint32_t)f[i][0], (uint32_t)f[i][1]});
+                    const v4i hi = bf16_of_fp8(v2u{(uint32_t)f[i][2], (uint32_t)f[i][3]});
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        s[n] = mfma32(lo, q[n][2 * k], s[n]);
+                        s[n] = mfma32(hi, q[n][2 * k + 1], s[n]);
+                    }
                 } else {
-                    s = mfma32(f[i], q[n], s);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        s[n] = mfma32(f[i], q[n][k], s[n]);
                 }
             }
         });
     });
-    return s;
 }
 
 // The running softmax's state of this lane's row
@@ -418,11 +427,13 @@ __device__ __forceinline__ v16f values_apart(const v4i (&w)[2], const v4i (&p)[2
     return sum;
 }
 
-// O^T += V^T P^T of one block.  masked (wave-uniform): some rows do not see
-// some of its keys; lo, hi: keys of the block that this lane's row sees.
-template <int DP, bool FP8>
-__device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND], uint32_t at, const v4i (&p)[2],
-                                       AttnState<AttnLds<DP, FP8>::ND> &t, bool masked, int lo, int hi, int lane)
+// O^T += V^T P^T of one block, for NT tiles of 32 rows.  masked (wave-uniform):
+// some rows do not see some of its keys; lo, hi: keys of the block that this
+// lane's row of a tile sees.
+template <int DP, bool FP8, int NT>
+__device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND], uint32_t at, const v4i (&p)[NT][2],
+                                       AttnState<AttnLds<DP, FP8>::ND> (&t)[NT], bool masked, const int (&lo)[NT],
+                                       const int (&hi)[NT], int lane)
 {
     using L = AttnLds<DP, FP8>;
     using V = AttnV<DP, FP8>;
@@ -445,15 +456,21 @@ __device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND
                 for (int e = 0; e < 8; ++e)
                     special |= special_pair(w[e >> 2][e & 3]);
                 if (__builtin_amdgcn_ballot_w64(special)) {
-                    const v16f x = values_apart(w, p, lo, hi, lane);
 #pragma unroll
-                    for (int g = 0; g < 16; ++g)
-                        t.o[D0 + I][g] += x[g];
+                    for (int n = 0; n < NT; ++n) {
+                        const v16f x = values_apart(w, p[n], lo[n], hi[n], lane);
+#pragma unroll
+                        for (int g = 0; g < 16; ++g)
+                            t[n].o[D0 + I][g] += x[g];
+                    }
                     w[0] = w[1] = v4i{0, 0, 0, 0};
                 }
             }
-            t.o[D0 + I] = mfma32(w[0], p[0], t.o[D0 + I]);
-            t.o[D0 + I] = mfma32(w[1], p[1], t.o[D0 + I]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                t[n].o[D0 + I] = mfma32(w[0], p[n][0], t[n].o[D0 + I]);
+                t[n].o[D0 + I] = mfma32(w[1], p[n][1], t[n].o[D0 + I]);
+            }
         });
     });
 }

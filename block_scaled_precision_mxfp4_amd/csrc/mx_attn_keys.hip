@@ -25,7 +25,7 @@ struct KeysShape {
     static constexpr int PER_CU = BYTES <= 65536 ? 2 : 1;
 };
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, int NT>
 __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_kernel(AttnArgs a, int mode)
 {
     using L = AttnLds<DP, FP8>;
@@ -33,15 +33,17 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     constexpr int NW = SH::NW, ST = SH::ST, STAGE = SH::STAGE;
     constexpr int NI = 2 * L::NIH;        // load instructions of a block of K, or of V
     constexpr int QC = DP / 8;            // 8-column pieces of a row
+    constexpr int TM = NT * kAttnTile;    // rows of a tile
+    static_assert(TM * DP * 4 <= ST * STAGE, "a wave's ring holds its rows of O");
     __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
-    __shared__ float s_ml[NW][32][2];
+    __shared__ float s_ml[NW][TM][2];
     __shared__ int s_last;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
     AttnPlan plan;
-    if (!attn_plan(a, kAttnTile, mode, wg, gridDim.x, lane, plan))
+    if (!attn_plan(a, TM, mode, wg, gridDim.x, lane, plan))
         return;
 
     uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
@@ -54,21 +56,21 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     const int end = min(at + plan.chunk, plan.total);
     int s = plan.s, seq_start = plan.start;
     AttnSeq q = plan.q;
-    int cost = seq_steps(a, q, kAttnTile, plan.per), units = seq_units(a, q, kAttnTile);
+    int cost = seq_steps(a, q, TM, plan.per), units = seq_units(a, q, TM);
     while (at < end) {
         while (at >= seq_start + units * cost) {
             seq_start += units * cost;
             if (++s >= a.c.seqs)
                 return;
             q = load_seq(a.c, a.T, s);
-            cost = seq_steps(a, q, kAttnTile, plan.per);
-            units = seq_units(a, q, kAttnTile);
+            cost = seq_steps(a, q, TM, plan.per);
+            units = seq_units(a, q, TM);
         }
         const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
         const int tile = u / a.c.kv_heads, head = u % a.c.kv_heads;
         const int piece_end = min(end, unit_start + cost);
         // its rows, and the keys that they see
-        const int r0 = tile * kAttnTile, rows = min(q.n * a.group - r0, kAttnTile);
+        const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
         int lo, hi;
         tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
@@ -99,64 +101,87 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             pg1 = attn_page(a.c, table, key0 + 16);
         };
 
-        AttnState<L::ND> t;
-        t.reset();
+        AttnState<L::ND> t[NT];
         const AttnScale sc = attn_scale(a, head);
         const int row = lane & 31;
-        const int idx = (r0 + min(row, rows - 1)) / a.group;  // the row's new token
-        const int pos = q.len - q.n + idx;
-        const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
-        const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        int idx[NT], row_lo[NT], row_hi[NT];  // this lane's row of each 32: its new token, the keys that it sees
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            t[n].reset();
+            idx[n] = (r0 + min(n * 32 + row, rows - 1)) / a.group;
+            const int pos = q.len - q.n + idx[n];
+            row_hi[n] = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
+            row_lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+        }
         if (nb > 0) {
             int pg0[ST], pg1[ST];
 #pragma unroll
             for (int i = 0; i < ST; ++i)
                 pages(i, pg0[i], pg1[i]);
-            v4i qf[L::NS];
-            {
-                const int hq = head * a.group + (r0 + row) % a.group;
-                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + hq * a.c.D, row < rows && !sc.zero, lane, qf);
+            v4i qf[NT][L::NS];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = n * 32 + row, hq = head * a.group + (r0 + min(r, rows - 1)) % a.group;
+                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx[n]) * a.ldq + hq * a.c.D, r < rows && !sc.zero, lane, qf[n]);
             }
 #pragma unroll
             for (int i = 0; i < ST - 1; ++i)
                 issue(i, pg0[i], pg1[i]);
             int next0 = pg0[ST - 1], next1 = pg1[ST - 1];
-            negate_q(qf, sc.negate);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                negate_q(qf[n], sc.negate);
             // keys that every row of the tile sees
-            const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 31) : 0;
-            const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
+            const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo[NT - 1], 31) : 0;
+            const int all_hi = __builtin_amdgcn_readlane(row_hi[0], 0);
             for (int i = 0; i < nb; ++i) {
                 issue(i + ST - 1, next0, next1);
                 pages(i + ST, next0, next1);
                 const uint32_t slot = (uint32_t)((i % ST) * STAGE);
                 const int key0 = (b0 + wave + i * NW) * 32;
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
-                v16f x[1] = {scores<DP, FP8>(ka, slot, qf)};
+                v16f x[NT];
+                scores<DP, FP8, NT>(ka, slot, qf, x);
                 const bool masked = key0 < all_lo || key0 + 32 > all_hi;
-                if (masked)
-                    mask_scores(x[0], row_lo - key0, row_hi - key0, lane);
-                v4i p[1][2];
-                softmax_blocks(t, x, sc.c, p);
+                int lo_b[NT], hi_b[NT];
+                v4i p[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    lo_b[n] = row_lo[n] - key0;
+                    hi_b[n] = row_hi[n] - key0;
+                    if (masked)
+                        mask_scores(x[n], lo_b[n], hi_b[n], lane);
+                    v16f y[1] = {x[n]};
+                    v4i w[1][2];
+                    softmax_blocks(t[n], y, sc.c, w);
+                    p[n][0] = w[0][0];
+                    p[n][1] = w[0][1];
+                }
                 attn_wait_vm<(ST - 1) * 2 * NI>();
-                values<DP, FP8>(va, slot, p[0], t, masked, row_lo - key0, row_hi - key0, lane);
+                values<DP, FP8, NT>(va, slot, p, t, masked, lo_b, hi_b, lane);
             }
         }
         // merge the waves: O to the wave's ring, rows of DP floats whose
         // 16-byte chunks are swizzled by the row
         attn_wait_vm<0>();
-        t.l = row_sum(t.l);
-        if (row < rows) {
-            float *o = reinterpret_cast<float *>(mine) + row * DP;
 #pragma unroll
-            for (int d = 0; d < L::ND; ++d)
+        for (int n = 0; n < NT; ++n) {
+            const int r = n * 32 + row;
+            t[n].l = row_sum(t[n].l);
+            if (r < rows) {
+                float *o = reinterpret_cast<float *>(mine) + r * DP;
 #pragma unroll
-                for (int g = 0; g < 16; g += 4) {
-                    const int ch = d * 8 + (g >> 2) * 2 + (lane >> 5);
-                    *reinterpret_cast<v4f *>(o + ((ch ^ (row & 15)) * 4)) = v4f{t.o[d][g], t.o[d][g + 1], t.o[d][g + 2], t.o[d][g + 3]};
+                for (int d = 0; d < L::ND; ++d)
+#pragma unroll
+                    for (int g = 0; g < 16; g += 4) {
+                        const int ch = d * 8 + (g >> 2) * 2 + (lane >> 5);
+                        *reinterpret_cast<v4f *>(o + ((ch ^ (r & 15)) * 4)) =
+                            v4f{t[n].o[d][g], t[n].o[d][g + 1], t[n].o[d][g + 2], t[n].o[d][g + 3]};
+                    }
+                if (lane < 32) {
+                    s_ml[wave][r][0] = t[n].m;
+                    s_ml[wave][r][1] = t[n].l;
                 }
-            if (lane < 32) {
-                s_ml[wave][row][0] = t.m;
-                s_ml[wave][row][1] = t.l;
             }
         }
         __syncthreads();
@@ -164,7 +189,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         // starts in it: its counter is that workgroup's), and this one's place for
         // a partial result
         const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
-        constexpr int FLOATS = 32 * (DP + 2);
+        constexpr int FLOATS = TM * (DP + 2);
         const __amdgpu_buffer_rsrc_t part = make_rsrc_u(
             a.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * FLOATS, FLOATS * 4);
         // what the waves have in LDS, added up: the result, or this workgroup's part of it
@@ -198,7 +223,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                     store16_coherent(part, (uint32_t)((r * DP + c8 * 8 + 4) * 4), v4f{o[4], o[5], o[6], o[7]});
                     if (c8 == 0)
                         __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(m), __float_as_uint(l)}, part,
-                                                              (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
+                                                              (uint32_t)((TM * DP + 2 * r) * 4), 0, kCoherent);
                 }
             }
         };
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                         for (int i = 0; i < PB; ++i) {
                             const int w = min(w0 + i * NW, parts - 1);  // (past the end: the last one, not added)
                             const uint32_t base = (uint32_t)w * (2 * FLOATS * 4) + (w == 0 ? off : 0);
-                            ml[i] = __builtin_amdgcn_raw_buffer_load_b64(all, base + (uint32_t)((32 * DP + 2 * r) * 4), 0, kCoherent);
+                            ml[i] = __builtin_amdgcn_raw_buffer_load_b64(all, base + (uint32_t)((TM * DP + 2 * r) * 4), 0, kCoherent);
                             x[i][0] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8) * 4));
                             x[i][1] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8 + 4) * 4));
                         }
@@ -261,33 +286,33 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     }
 }
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, int NT>
 void launch(const AttnArgs &a, int plan, int grid, hipStream_t s)
 {
-    mx_attn_keys_kernel<DP, FP8><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a, plan);
+    mx_attn_keys_kernel<DP, FP8, NT><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a, plan);
+}
+
+template <int DP, bool FP8>
+constexpr AttnKeysKernel entry()
+{
+    if constexpr (DP < 256)
+        return {KeysShape<DP, FP8>::PER_CU, {launch<DP, FP8, 1>, launch<DP, FP8, 2>}};
+    else
+        return {KeysShape<DP, FP8>::PER_CU, {launch<DP, FP8, 1>, nullptr}};
 }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 }  // namespace
 
-int64_t attn_partial_floats(int D) { return 32 * ((int64_t)padded(D) + 4); }  // (rows: an m and l per lane)
+int64_t attn_partial_floats(int D) { return 32 * ((int64_t)padded(D) + 4); }  // (the rows kernel's: an m and l per lane)
 
-int attn_keys_per_cu(int D, bool fp8)
+AttnKeysKernel attn_keys_kernel(int D, bool fp8)
 {
     switch (padded(D)) {
-    case 64: return fp8 ? KeysShape<64, true>::PER_CU : KeysShape<64, false>::PER_CU;
-    case 128: return fp8 ? KeysShape<128, true>::PER_CU : KeysShape<128, false>::PER_CU;
-    default: return fp8 ? KeysShape<256, true>::PER_CU : KeysShape<256, false>::PER_CU;
-    }
-}
-
-void launch_attn_keys(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
-{
-    switch (padded(a.c.D)) {
-    case 64: return fp8 ? launch<64, true>(a, plan, grid, s) : launch<64, false>(a, plan, grid, s);
-    case 128: return fp8 ? launch<128, true>(a, plan, grid, s) : launch<128, false>(a, plan, grid, s);
-    default: return fp8 ? launch<256, true>(a, plan, grid, s) : launch<256, false>(a, plan, grid, s);
+    case 64: return fp8 ? entry<64, true>() : entry<64, false>();
+    case 128: return fp8 ? entry<128, true>() : entry<128, false>();
+    default: return fp8 ? entry<256, true>() : entry<256, false>();
     }
 }
 

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
             }
         };
 
-        AttnState<L::ND> t;
+        AttnState<L::ND> ts[1];
+        AttnState<L::ND> &t = ts[0];
         t.reset();
         const AttnScale sc = attn_scale(a, head);
         const int w0 = r0 + wave * 32, wrows = min(max(rows - wave * 32, 0), 32);  // this wave's rows
@@ -136,10 +137,10 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
         const int any_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 0) : 0;
         const int any_hi = wrows > 0 ? __builtin_amdgcn_readlane(row_hi, 31) : 0;
-        v4i qf[L::NS];
+        v4i qf[1][L::NS];
         load_q<DP, false>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + (head * a.group + rr % a.group) * a.c.D,
-                          row < wrows && !sc.zero, lane, qf);
-        negate_q(qf, sc.negate);
+                          row < wrows && !sc.zero, lane, qf[0]);
+        negate_q(qf[0], sc.negate);
         if (nt > 0) {
             constexpr int AHEAD = ST - 1;
             if constexpr (FP8) {
@@ -169,8 +170,11 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
                     continue;
                 v16f x[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    x[b] = scores<DP, false>(ka, slot + b * L::BLOCK, qf);
+                for (int b = 0; b < NB; ++b) {
+                    v16f y[1];
+                    scores<DP, false, 1>(ka, slot + b * L::BLOCK, qf, y);
+                    x[b] = y[0];
+                }
                 const bool masked = key < all_lo || key + KT > all_hi;
                 if (masked)
 #pragma unroll
@@ -179,8 +183,11 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
                 v4i p[NB][2];
                 softmax_blocks(t, x, sc.c, p);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    values<DP, false>(va, slot + b * L::BLOCK, p[b], t, masked, row_lo - key - 32 * b, row_hi - key - 32 * b, lane);
+                for (int b = 0; b < NB; ++b) {
+                    const v4i pb[1][2] = {{p[b][0], p[b][1]}};
+                    const int bl[1] = {row_lo - key - 32 * b}, bh[1] = {row_hi - key - 32 * b};
+                    values<DP, false, 1>(va, slot + b * L::BLOCK, pb, ts, masked, bl, bh, lane);
+                }
             }
         }
         attn_wait_vm<0>();

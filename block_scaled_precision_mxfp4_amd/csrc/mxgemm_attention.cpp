@@ -17,7 +17,7 @@ constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxSeqs = 1 << 16;
 constexpr int kMaxHeads = 512;  // of queries, keys and values together
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
-constexpr int kKeysRows = 32;   // rows of a sequence and key head up to which its waves share a tile
+constexpr int kKeysRows = 64;   // rows of a sequence and key head up to which its waves share a tile
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -141,7 +141,7 @@ size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv
 {
     if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
         return 0;
-    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::attn_rows_tile(head_dim) / 32 : 1;
+    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::attn_rows_tile(head_dim) / 32 : 2;
     return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * parts * mx::attn_partial_floats(head_dim) * 4);
 }
 
@@ -200,16 +200,20 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     a.partials = (float *)((uint8_t *)workspace + mx::kAttnCounterBytes);
     const bool fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
     const int most_new = p->max_new > 0 ? std::min(p->max_new, T) : T;
-    const bool rows = (int64_t)most_new * G > kKeysRows;
-    const int64_t tiles = rows ? most_units(T, cache->seqs, G, Hk, mx::attn_rows_tile(D)) : units;
-    const int64_t wgs = std::min<int64_t>((int64_t)cu * (rows ? mx::attn_rows_per_cu(D) : mx::attn_keys_per_cu(D, fp8)), mx::kAttnPieces);
-    if (rows) {
+    const mx::AttnKeysKernel keys = mx::attn_keys_kernel(D, fp8);
+    const int64_t most_rows = (int64_t)most_new * G;
+    const int tile = most_rows <= mx::kAttnTile || !keys.launch[1] ? mx::kAttnTile : 2 * mx::kAttnTile;
+    if (most_rows > kKeysRows) {
+        const int64_t tiles = most_units(T, cache->seqs, G, Hk, mx::attn_rows_tile(D));
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * mx::attn_rows_per_cu(D), mx::kAttnPieces);
         if (tiles >= 2 * wgs)
             mx::launch_attn_rows(a, fp8, mx::kPlanWhole, (int)tiles, stream);
         else
             mx::launch_attn_rows(a, fp8, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     } else {
-        mx::launch_attn_keys(a, fp8, 2 * tiles <= wgs ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
+        const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * keys.per_cu, mx::kAttnPieces);
+        keys.launch[tile / mx::kAttnTile - 1](a, 2 * tiles <= wgs ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     }
     return launched();
 }
