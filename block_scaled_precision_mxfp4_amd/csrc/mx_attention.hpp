@@ -22,6 +22,21 @@ struct CacheArgs {
     int D;
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: d > 1 takes s = ceil(log2 d), m =
+// ceil(2^(31 + s) / d) and (n * m) >> (31 + s), off by n (m d - 2^(31 + s)) / (d
+// 2^(31 + s)) < 1 / d; m = 0 stands for d = 1.
+struct Divisor {
+    uint32_t m;
+    int shift;  // s - 1, behind the high word
+};
+inline Divisor divisor(int d)
+{
+    int s = 0;
+    while (((int64_t)1 << s) < d)
+        ++s;
+    return d > 1 ? Divisor{(uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), s - 1} : Divisor{0, 0};
+}
+
 // ---- append (mx_append.hip)
 struct AppendArgs {
     CacheArgs c;
@@ -51,6 +66,7 @@ struct AttnArgs {
     int64_t ldq, ldo, lda_b, lds;
     float scale;
     int T, heads, group;     // group: query heads of a key head
+    Divisor by_group, by_kv_heads;
     int causal, window, a_fp8;
     int *counters;           // [kAttnPieces], zero between calls
     float *partials;
@@ -59,7 +75,7 @@ struct AttnArgs {
 // compute unit; tiles of 32 and of 64 rows (may be null).
 typedef void (*AttnLaunchFn)(const AttnArgs &, int plan, int grid, hipStream_t);
 struct AttnKeysKernel {
-    int per_cu;
+    int per_cu[2];
     AttnLaunchFn launch[2];
 };
 AttnKeysKernel attn_keys_kernel(int D, bool fp8);

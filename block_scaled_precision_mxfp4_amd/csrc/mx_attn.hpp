@@ -103,6 +103,18 @@ __device__ __forceinline__ float load_uniform(const float *p)
     return *(const __attribute__((address_space(4))) float *)(uintptr_t)p;
 }
 
+__device__ __forceinline__ int quotient(int n, Divisor d) { return d.m ? (int)(__umulhi((uint32_t)n, d.m) >> d.shift) : n; }
+
+// A row of a sequence: its new token, its query head
+struct AttnRow {
+    int token, head;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs &a, int r, int kv_head)
+{
+    const int t = quotient(r, a.by_group);
+    return {t, kv_head * a.group + (r - t * a.group)};
+}
+
 // ---- sequences
 
 struct AttnSeq {
@@ -227,23 +239,58 @@ struct AttnLds {
     }
 };
 
-// 16 keys from key0 on of one key head: descriptors of K's and V's rows that
-// exist (the others read as zeros).  page: the page's index as the table has it.
+// 16 keys from key0 on: descriptors of K's and V's rows that exist (the others
+// read as zeros).  k, v: the key head's rows in page 0.  page: as the table has it.
 struct AttnRows {
     __amdgpu_buffer_rsrc_t k, v;
 };
-__device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, int head, int page, int key0, int len)
+__device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, const uint8_t *k, const uint8_t *v, int page, int key0, int len)
 {
     const bool there = (uint32_t)page < (uint32_t)c.num_pages;
     const int rows = there ? min(max(len - key0, 0), 16) : 0;
-    const int64_t at = (int64_t)(there ? page : 0) * c.page_b + head * c.head_b +
-                       (int64_t)(key0 & ((1 << c.page_shift) - 1)) * c.token_b;
+    const int64_t at = (int64_t)(there ? page : 0) * c.page_b + (uint32_t)(key0 & ((1 << c.page_shift) - 1)) * (uint32_t)c.token_b;
     const uint32_t bytes = (uint32_t)rows * (uint32_t)c.token_b;
-    return {make_rsrc_u(c.k + at, bytes), make_rsrc_u(c.v + at, bytes)};
+    return {make_rsrc_u(k + at, bytes), make_rsrc_u(v + at, bytes)};
 }
-__device__ __forceinline__ int attn_page(const CacheArgs &c, const int32_t *table, int key0)
+
+// A sequence's page table, 64 entries at a time in a register (an entry per
+// lane) and the next 64 on their way: a scalar load per block would be waited
+// for together with the LDS reads behind it.
+struct AttnPages {
+    const int32_t *table;
+    int first, last;  // entry of lane 0; the table's last one
+    int ids, next;
+    __device__ __forceinline__ int load(int at, int lane) const { return table[min(at + lane, last)]; }
+    __device__ __forceinline__ void open(const CacheArgs &c, int s, int at, int lane)
+    {
+        table = c.pages + (int64_t)s * c.ld_pages;
+        last = c.max_pages - 1;
+        first = at;
+        ids = load(at, lane);
+        next = load(at + 64, lane);
+    }
+    // at: wave-uniform, from one call to the next by less than 64 upwards
+    __device__ __forceinline__ int page(int at, int lane)
+    {
+        if (at >= first + 64) {
+            first += 64;
+            ids = next;
+            next = load(first + 64, lane);
+        }
+        return __builtin_amdgcn_readlane(ids, at - first);
+    }
+};
+
+// The kernel's arguments read again: fields that only the end of a unit needs
+// would else be kept in scalar registers over its loop (100 of them spilled).
+__device__ __forceinline__ AttnArgs args_again()
 {
-    return load_uniform(table + min(key0 >> c.page_shift, c.max_pages - 1));
+    const __attribute__((address_space(4))) AttnArgs *p =
+        (const __attribute__((address_space(4))) AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    AttnArgs a;
+    __builtin_memcpy(&a, (const AttnArgs *)p, sizeof a);
+    return a;
 }
 
 // ---- products and softmax
@@ -554,7 +601,8 @@ __device__ __forceinline__ void finish_tile(const AttnArgs &a, const AttnSeq &q,
 {
     constexpr int CH = DP / 8;  // 16-byte chunks of a row
     const int row = lane & 31, rr = r0 + min(row, rows - 1);
-    const int token = q.t0 + rr / a.group, head = kv_head * a.group + rr % a.group;
+    const AttnRow at = attn_row(a, rr, kv_head);
+    const int token = q.t0 + at.token, head = at.head;
     const RowEnd e = end_row(a, kv_head, head, m, l);
     if (a.lse && lane < rows)
         a.lse[(int64_t)token * a.heads + head] = e.lse;
@@ -573,8 +621,8 @@ __device__ __forceinline__ void finish_tile(const AttnArgs &a, const AttnSeq &q,
     for (int i = 0; i < 32 * CH / 64; ++i) {
         const int r = (i * 64 + lane) / CH, c = lane % CH;
         const v4i x = *reinterpret_cast<const v4i *>(lds + r * (DP * 2) + ((c ^ swz(r)) * 16));
-        const int r1 = r0 + min(r, rows - 1);
-        store_row(a, q.t0 + r1 / a.group, kv_head * a.group + r1 % a.group, c * 8, x, r < rows && c * 8 < a.c.D);
+        const AttnRow to = attn_row(a, r0 + min(r, rows - 1), kv_head);
+        store_row(a, q.t0 + to.token, to.head, c * 8, x, r < rows && c * 8 < a.c.D);
     }
 }
 

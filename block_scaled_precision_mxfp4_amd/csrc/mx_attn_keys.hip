@@ -42,9 +42,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
-    AttnPlan plan;
-    if (!attn_plan(a, TM, mode, wg, gridDim.x, lane, plan))
-        return;
+    const AttnFirst first_loads = attn_first(a, lane);
 
     uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
     L::load_offsets(a.c, lane, ko, vo);
@@ -52,6 +50,9 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     L::k_addr(lds_addr(mine), lane, ka);
     L::v_addr(lds_addr(mine) + L::BLOCK, lane, va);
 
+    AttnPlan plan;
+    if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+        return;
     int at = wg * plan.chunk;
     const int end = min(at + plan.chunk, plan.total);
     int s = plan.s, seq_start = plan.start;
@@ -67,20 +68,23 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             units = seq_units(a, q, TM);
         }
         const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
-        const int tile = u / a.c.kv_heads, head = u % a.c.kv_heads;
+        const int tile = quotient(u, a.by_kv_heads), head = u - tile * a.c.kv_heads;
         const int piece_end = min(end, unit_start + cost);
         // its rows, and the keys that they see
         const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
         int lo, hi;
-        tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
+        tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
         const int b0 = max(keys.lo, lo) / 32, b1 = (keys.hi + 31) / 32;
         const int nb = max((b1 - b0 - wave + NW - 1) / NW, 0);  // this wave's blocks: b0 + wave, + NW, ...
 
-        const int32_t *table = a.c.pages + (int64_t)s * a.c.ld_pages;
-        auto issue = [&](int i, int pg0, int pg1) __attribute__((always_inline)) {
+        const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
+        AttnPages table;
+        auto issue = [&](int i) __attribute__((always_inline)) {
             const int key0 = (b0 + wave + i * NW) * 32, len = i < nb ? q.len : 0;
-            const AttnRows x = attn_rows(a.c, head, pg0, key0, len), y = attn_rows(a.c, head, pg1, key0 + 16, len);
+            const int pg0 = table.page(key0 >> a.c.page_shift, lane), pg1 = table.page((key0 + 16) >> a.c.page_shift, lane);
+            const AttnRows x = attn_rows(a.c, k_head, v_head, pg0, key0, len);
+            const AttnRows y = attn_rows(a.c, k_head, v_head, pg1, key0 + 16, len);
             uint8_t *to = mine + (i % ST) * STAGE;
 #pragma unroll
             for (int j = 0; j < L::NIH; ++j)
@@ -95,39 +99,30 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             for (int j = 0; j < L::NIH; ++j)
                 load16_to_lds_stream(y.v, (lds_void *)(to + L::BLOCK + L::BLOCK / 2 + j * 1024), vo[j]);
         };
-        auto pages = [&](int i, int &pg0, int &pg1) __attribute__((always_inline)) {
-            const int key0 = (b0 + wave + i * NW) * 32;
-            pg0 = attn_page(a.c, table, key0);
-            pg1 = attn_page(a.c, table, key0 + 16);
-        };
 
         AttnState<L::ND> t[NT];
         const AttnScale sc = attn_scale(a, head);
         const int row = lane & 31;
-        int idx[NT], row_lo[NT], row_hi[NT];  // this lane's row of each 32: its new token, the keys that it sees
+        AttnRow my[NT];  // this lane's row of each 32, and the keys that it sees
+        int row_lo[NT], row_hi[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             t[n].reset();
-            idx[n] = (r0 + min(n * 32 + row, rows - 1)) / a.group;
-            const int pos = q.len - q.n + idx[n];
+            my[n] = attn_row(a, r0 + min(n * 32 + row, rows - 1), head);
+            const int pos = q.len - q.n + my[n].token;
             row_hi[n] = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
             row_lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
         }
         if (nb > 0) {
-            int pg0[ST], pg1[ST];
-#pragma unroll
-            for (int i = 0; i < ST; ++i)
-                pages(i, pg0[i], pg1[i]);
+            table.open(a.c, s, ((b0 + wave) * 32) >> a.c.page_shift, lane);
             v4i qf[NT][L::NS];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int r = n * 32 + row, hq = head * a.group + (r0 + min(r, rows - 1)) % a.group;
-                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + idx[n]) * a.ldq + hq * a.c.D, r < rows && !sc.zero, lane, qf[n]);
+                load_q<DP, FP8>(a, a.Q + (int64_t)(q.t0 + my[n].token) * a.ldq + my[n].head * a.c.D, n * 32 + row < rows && !sc.zero, lane, qf[n]);
             }
 #pragma unroll
             for (int i = 0; i < ST - 1; ++i)
-                issue(i, pg0[i], pg1[i]);
-            int next0 = pg0[ST - 1], next1 = pg1[ST - 1];
+                issue(i);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 negate_q(qf[n], sc.negate);
@@ -135,8 +130,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo[NT - 1], 31) : 0;
             const int all_hi = __builtin_amdgcn_readlane(row_hi[0], 0);
             for (int i = 0; i < nb; ++i) {
-                issue(i + ST - 1, next0, next1);
-                pages(i + ST, next0, next1);
+                issue(i + ST - 1);
                 const uint32_t slot = (uint32_t)((i % ST) * STAGE);
                 const int key0 = (b0 + wave + i * NW) * 32;
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
@@ -164,6 +158,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         // merge the waves: O to the wave's ring, rows of DP floats whose
         // 16-byte chunks are swizzled by the row
         attn_wait_vm<0>();
+        const AttnArgs e = args_again();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = n * 32 + row;
@@ -191,12 +186,16 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
         constexpr int FLOATS = TM * (DP + 2);
         const __amdgpu_buffer_rsrc_t part = make_rsrc_u(
-            a.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * FLOATS, FLOATS * 4);
+            e.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * FLOATS, FLOATS * 4);
+        auto finish_unit_row = [&](int r, int c8, float m, float l, const float (&o)[8], bool live) __attribute__((always_inline)) {
+            const AttnRow to = attn_row(e, r0 + r, head);
+            finish_row(e, head, q.t0 + to.token, to.head, c8 * 8, m, l, [&](int i) { return o[i]; }, live);
+        };
         // what the waves have in LDS, added up: the result, or this workgroup's part of it
         auto merge = [&](bool result) __attribute__((always_inline)) {
             for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
                 const int r = it / QC, c8 = it % QC;
-                const bool live = r < rows && c8 * 8 < a.c.D;
+                const bool live = r < rows && c8 * 8 < e.c.D;
                 const int rr = min(r, rows - 1);
                 float m = kNegInf, l = 0.0f, o[8] = {};
 #pragma unroll
@@ -211,13 +210,12 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                     for (int h = 0; h < 2; ++h) {
                         const v4f x = *reinterpret_cast<const v4f *>(src + (((2 * c8 + h) ^ (rr & 15)) * 4));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[4 * h + e] += f * x[e];
+                        for (int i = 0; i < 4; ++i)
+                            o[4 * h + i] += f * x[i];
                     }
                 }
                 if (result) {
-                    const int i = (r0 + rr) / a.group;
-                    finish_row(a, head, q.t0 + i, head * a.group + (r0 + rr) % a.group, c8 * 8, m, l, [&](int e) { return o[e]; }, live);
+                    finish_unit_row(rr, c8, m, l, o, live);
                 } else if (live) {
                     store16_coherent(part, (uint32_t)((r * DP + c8 * 8) * 4), v4f{o[0], o[1], o[2], o[3]});
                     store16_coherent(part, (uint32_t)((r * DP + c8 * 8 + 4) * 4), v4f{o[4], o[5], o[6], o[7]});
@@ -230,53 +228,69 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         bool done = first == last;
         if (!done) {
             merge(false);
-            done = split_arrive_last_via(a.counters + first, last - first + 1, &s_last);
+            done = split_arrive_last_via(e.counters + first, last - first + 1, &s_last);
             if (done) {
-                // each wave adds up every NW-th part, PB of them in flight, into
-                // its ring.  The first workgroup's part of this unit is its last
-                // one unless the unit starts with it; the others' is their first
-                constexpr int PB = 8;
-                const __amdgpu_buffer_rsrc_t all =
-                    make_rsrc_u(a.partials + 2 * (int64_t)first * FLOATS, (uint32_t)(last - first + 1) * (2 * FLOATS * 4));
-                const uint32_t off = unit_start > first * plan.chunk ? FLOATS * 4 : 0;
+                // The first workgroup's part of this unit is its last one unless the
+                // unit starts with it; the others' is their first
+                constexpr int PB = 8;  // parts in flight
                 const int parts = last - first + 1;
-                for (int it = lane; it < rows * QC; it += 64) {
-                    const int r = it / QC, c8 = it % QC;
-                    float m = kNegInf, l = 0.0f, o[8] = {};
-                    for (int w0 = wave; w0 < parts; w0 += NW * PB) {
+                const __amdgpu_buffer_rsrc_t all = make_rsrc_u(e.partials + 2 * (int64_t)first * FLOATS, (uint32_t)parts * (2 * FLOATS * 4));
+                const uint32_t off = unit_start > first * plan.chunk ? FLOATS * 4 : 0;
+                // parts from, from + step, ... of one piece of a row
+                auto add_parts = [&](int r, int c8, int from, int step, float &m, float &l, float (&o)[8]) __attribute__((always_inline)) {
+                    for (int w0 = from; w0 < parts; w0 += step * PB) {
                         v2u ml[PB];
                         v4f x[PB][2];
 #pragma unroll
                         for (int i = 0; i < PB; ++i) {
-                            const int w = min(w0 + i * NW, parts - 1);  // (past the end: the last one, not added)
-                            const uint32_t base = (uint32_t)w * (2 * FLOATS * 4) + (w == 0 ? off : 0);
-                            ml[i] = __builtin_amdgcn_raw_buffer_load_b64(all, base + (uint32_t)((TM * DP + 2 * r) * 4), 0, kCoherent);
-                            x[i][0] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8) * 4));
-                            x[i][1] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8 + 4) * 4));
+                            const int w = w0 + i * step;
+                            if (w < parts) {
+                                const uint32_t base = (uint32_t)w * (2 * FLOATS * 4) + (w == 0 ? off : 0);
+                                ml[i] = __builtin_amdgcn_raw_buffer_load_b64(all, base + (uint32_t)((TM * DP + 2 * r) * 4), 0, kCoherent);
+                                x[i][0] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8) * 4));
+                                x[i][1] = load16_coherent(all, base + (uint32_t)((r * DP + c8 * 8 + 4) * 4));
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < PB; ++i) {
-                            if (w0 + i * NW >= parts)
-                                break;
-                            const float mw = __uint_as_float(ml[i][0]), n = fmaxf(m, mw);
-                            const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
-                            m = n;
-                            l = l * f0 + __uint_as_float(ml[i][1]) * f1;
+                            if (w0 + i * step < parts) {
+                                const float mw = __uint_as_float(ml[i][0]), n = fmaxf(m, mw);
+                                const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
+                                m = n;
+                                l = l * f0 + __uint_as_float(ml[i][1]) * f1;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                o[e] = o[e] * f0 + x[i][e >> 2][e & 3] * f1;
+                                for (int k = 0; k < 8; ++k)
+                                    o[k] = o[k] * f0 + x[i][k >> 2][k & 3] * f1;
+                            }
                         }
                     }
-                    float *dst = reinterpret_cast<float *>(mine) + r * DP;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<v4f *>(dst + (((2 * c8 + h) ^ (r & 15)) * 4)) = v4f{o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
-                    if (c8 == 0) {
-                        s_ml[wave][r][0] = m;
-                        s_ml[wave][r][1] = l;
+                };
+                if (parts <= PB) {
+                    // few parts: every thread adds up its own pieces of rows
+                    for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
+                        const int r = min(it / QC, rows - 1), c8 = it % QC;
+                        float m = kNegInf, l = 0.0f, o[8] = {};
+                        add_parts(r, c8, 0, 1, m, l, o);
+                        finish_unit_row(r, c8, m, l, o, it / QC < rows && c8 * 8 < e.c.D);
                     }
+                    done = false;
+                } else {
+                    // each wave adds up every NW-th one, into its ring
+                    for (int it = lane; it < rows * QC; it += 64) {
+                        const int r = it / QC, c8 = it % QC;
+                        float m = kNegInf, l = 0.0f, o[8] = {};
+                        add_parts(r, c8, wave, NW, m, l, o);
+                        float *dst = reinterpret_cast<float *>(mine) + r * DP;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<v4f *>(dst + (((2 * c8 + h) ^ (r & 15)) * 4)) = v4f{o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
+                        if (c8 == 0) {
+                            s_ml[wave][r][0] = m;
+                            s_ml[wave][r][1] = l;
+                        }
+                    }
+                    __syncthreads();
                 }
-                __syncthreads();
             }
         }
         if (done)
@@ -296,9 +310,9 @@ template <int DP, bool FP8>
 constexpr AttnKeysKernel entry()
 {
     if constexpr (DP < 256)
-        return {KeysShape<DP, FP8>::PER_CU, {launch<DP, FP8, 1>, launch<DP, FP8, 2>}};
+        return {{KeysShape<DP, FP8>::PER_CU, 1}, {launch<DP, FP8, 1>, launch<DP, FP8, 2>}};
     else
-        return {KeysShape<DP, FP8>::PER_CU, {launch<DP, FP8, 1>, nullptr}};
+        return {{KeysShape<DP, FP8>::PER_CU, 1}, {launch<DP, FP8, 1>, nullptr}};
 }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }

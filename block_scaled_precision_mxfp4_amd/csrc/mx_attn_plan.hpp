@@ -59,10 +59,24 @@ __device__ __forceinline__ KeyRange step_keys(int lo, int hi, int from, int to, 
     return {(int)min(k0, (int64_t)hi), (int)min(k1, (int64_t)hi)};
 }
 
+// The first loads of attn_plan, to be under way while the workgroup does
+// something else
+struct AttnFirst {
+    int o0, o1, len;
+};
+__device__ __forceinline__ AttnFirst attn_first(const AttnArgs &a, int lane)
+{
+    AttnFirst f = {0, 0, 0};
+    if (a.c.seqs <= 64 && lane < a.c.seqs)
+        f = {a.c.offsets[lane], a.c.offsets[lane + 1], a.c.lens[lane]};
+    return f;
+}
+
 // By one wave, the same result in every lane: the plan, and where workgroup
 // `wg` of `wgs` starts.  False: it has nothing (or the offsets count more than T
 // tokens, as those that do not ascend may).
-__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int mode, int wg, int wgs, int lane, AttnPlan &p)
+__device__ __forceinline__ bool attn_plan(const AttnArgs &a, const AttnFirst &f, int tile, int mode, int wg, int wgs, int lane,
+                                          AttnPlan &p)
 {
     const int S = a.c.seqs;
     const int each = (S + 63) / 64;  // sequences of a lane, in order
@@ -72,7 +86,7 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int tile, int mode,
     for (int i = 0; i < each; ++i) {
         const int s = lane * each + i;
         if (s < S) {
-            q = seq_of_lane(a, s);
+            q = each == 1 ? seq_from(a.c, a.T, f.o0, f.o1, f.len) : seq_of_lane(a, s);
             const int u = seq_units(a, q, tile);
             units += u;
             steps += u * seq_steps(a, q, tile, p.per);

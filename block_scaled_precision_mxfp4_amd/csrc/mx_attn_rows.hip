@@ -34,9 +34,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
-    AttnPlan plan;
-    if (!attn_plan(a, TM, mode, wg, gridDim.x, lane, plan))
-        return;
+    const AttnFirst first_loads = attn_first(a, lane);
 
     // this lane's places in the cache's rows and in a stage
     uint32_t ko[FP8 ? PPW : IPW], vo[FP8 ? PPW : IPW], kw[FP8 ? PPW : 1], vw[FP8 ? PPW : 1];
@@ -62,6 +60,9 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
     L::k_addr(lds_addr(ring), lane, ka);
     L::v_addr(lds_addr(ring) + KT * L::ROWB, lane, va);
 
+    AttnPlan plan;
+    if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+        return;
     int at = wg * plan.chunk;
     const int end = min(at + plan.chunk, plan.total);
     int s = plan.s, seq_start = plan.start;
@@ -78,24 +79,25 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         }
         const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
         // the tiles with the most keys first
-        const int tile = units / a.c.kv_heads - 1 - u / a.c.kv_heads, head = u % a.c.kv_heads;
+        const int nth = quotient(u, a.by_kv_heads), head = u - nth * a.c.kv_heads;
+        const int tile = seq_tiles(q, a.group, TM) - 1 - nth;
         const int piece_end = min(end, unit_start + cost);
         const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
         int lo, hi;
-        tile_keys(a, q, r0 / a.group, (r0 + rows - 1) / a.group, lo, hi);
+        tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
         const int k0 = max(keys.lo, lo / KT * KT), k1 = keys.hi;
         const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
 
-        const int32_t *table = a.c.pages + (int64_t)s * a.c.ld_pages;
+        const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
         const int my_key = k0 + (wave >> 1) * 16;  // the 16 keys that this wave's rows are among
-        int page = attn_page(a.c, table, my_key);
+        AttnPages table;
+        table.open(a.c, s, my_key >> a.c.page_shift, lane);
         v2u kr[PPW], vr[PPW];
         // loads of stage i: into LDS, or (8 bits) into registers
         auto issue = [&](int i) __attribute__((always_inline)) {
             const int key = my_key + i * KT;
-            const AttnRows x = attn_rows(a.c, head, page, key, i < nt ? q.len : 0);
-            page = attn_page(a.c, table, key + KT);
+            const AttnRows x = attn_rows(a.c, k_head, v_head, table.page(key >> a.c.page_shift, lane), key, i < nt ? q.len : 0);
             if constexpr (FP8) {
 #pragma unroll
                 for (int j = 0; j < PPW; ++j) {
@@ -129,7 +131,8 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const int w0 = r0 + wave * 32, wrows = min(max(rows - wave * 32, 0), 32);  // this wave's rows
         const int row = lane & 31;
         const int rr = w0 + min(row, max(wrows - 1, 0));
-        const int idx = rr / a.group, pos = q.len - q.n + idx;
+        const AttnRow my = attn_row(a, rr, head);
+        const int idx = my.token, pos = q.len - q.n + idx;
         const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
         const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
         // keys that every row of the wave sees, and that some see
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const int any_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 0) : 0;
         const int any_hi = wrows > 0 ? __builtin_amdgcn_readlane(row_hi, 31) : 0;
         v4i qf[1][L::NS];
-        load_q<DP, false>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + (head * a.group + rr % a.group) * a.c.D,
+        load_q<DP, false>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + my.head * a.c.D,
                           row < wrows && !sc.zero, lane, qf[0]);
         negate_q(qf[0], sc.negate);
         if (nt > 0) {
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
             }
         }
         attn_wait_vm<0>();
+        const AttnArgs end_args = args_again();
         t.l = row_sum(t.l);
         __syncthreads();  // the ring is free
         const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
             // a partial result: a wave's registers as they are
             constexpr int64_t PW = 64 * (L::ND * 16 + 2);  // floats of a wave
             const __amdgpu_buffer_rsrc_t to =
-                make_rsrc_u(a.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * (NW * PW) + wave * PW, PW * 4);
+                make_rsrc_u(end_args.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * (NW * PW) + wave * PW, PW * 4);
             if (wrows > 0) {
 #pragma unroll
                 for (int d = 0; d < L::ND; ++d)
@@ -210,13 +214,13 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
                 __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(t.m), __float_as_uint(t.l)}, to,
                                                       (uint32_t)(L::ND * 16 * 256 + lane * 8), 0, kCoherent);
             }
-            done = split_arrive_last_via(a.counters + first, last - first + 1, &s_last);
+            done = split_arrive_last_via(end_args.counters + first, last - first + 1, &s_last);
             if (done && wrows > 0) {
                 const int off = unit_start > first * plan.chunk ? 1 : 0;
                 t.reset();
                 for (int w = 0; w <= last - first; ++w) {
                     const __amdgpu_buffer_rsrc_t from = make_rsrc_u(
-                        a.partials + (2 * (int64_t)(first + w) + (w == 0 ? off : 0)) * (NW * PW) + wave * PW, PW * 4);
+                        end_args.partials + (2 * (int64_t)(first + w) + (w == 0 ? off : 0)) * (NW * PW) + wave * PW, PW * 4);
                     const v2u ml = __builtin_amdgcn_raw_buffer_load_b64(from, (uint32_t)(L::ND * 16 * 256 + lane * 8), 0, kCoherent);
                     const float mw = __uint_as_float(ml[0]), n = fmaxf(t.m, mw);
                     const float f0 = n == kNegInf ? 1.0f : exp2_fast(t.m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
             }
         }
         if (done && wrows > 0)
-            finish_tile<DP>(a, q, head, w0, wrows, t.m, t.l, t.o, ring + wave * (32 * DP * 2), lane);
+            finish_tile<DP>(end_args, q, head, w0, wrows, t.m, t.l, t.o, ring + wave * (32 * DP * 2), lane);
         __syncthreads();  // the ring is free again
         at = piece_end;
     }

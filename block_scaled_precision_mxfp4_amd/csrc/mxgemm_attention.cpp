@@ -69,7 +69,7 @@ int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
 bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 {
     return T >= 1 && T <= kMaxTokens && seqs >= 1 && seqs <= kMaxSeqs && kv_heads >= 1 && heads >= kv_heads &&
-           heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && D >= 32 && D <= 256 && D % 32 == 0;
+           heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && (int64_t)T * (heads / kv_heads) <= kMaxInt / 2 && D >= 32 && D <= 256 && D % 32 == 0;
 }
 
 }  // namespace
@@ -193,6 +193,8 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     a.T = T;
     a.heads = H;
     a.group = G;
+    a.by_group = mx::divisor(G);
+    a.by_kv_heads = mx::divisor(Hk);
     a.causal = p->causal;
     a.window = p->window;
     a.a_fp8 = bits == 8;
@@ -212,7 +214,7 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
             mx::launch_attn_rows(a, fp8, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     } else {
         const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
-        const int64_t wgs = std::min<int64_t>((int64_t)cu * keys.per_cu, mx::kAttnPieces);
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * keys.per_cu[tile / mx::kAttnTile - 1], mx::kAttnPieces);
         keys.launch[tile / mx::kAttnTile - 1](a, 2 * tiles <= wgs ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     }
     return launched();
