@@ -27,7 +27,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # Options of single sources.  Attention: matrix results in the vector registers
 # that the softmax works on; the compiler's choice was to move every accumulator
 # to the accumulation registers and back for each block of keys.
-SOURCE_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for name in ("mx_attn_keys.hip", "mx_attn_rows.hip")}
+SOURCE_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for name in ("mx_attn_keys.hip", "mx_attn_rows.hip", "mx_attn_rows_wide.hip")}
 
 
 def hipcc() -> str:

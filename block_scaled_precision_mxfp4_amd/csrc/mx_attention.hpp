@@ -81,10 +81,11 @@ struct AttnKeysKernel {
 AttnKeysKernel attn_keys_kernel(int D, bool fp8);
 // Floats of 32 rows of a partial result, at most
 int64_t attn_partial_floats(int D);
-// The kernel whose waves hold 32 rows each (mx_attn_rows.hip): rows of its
+// The kernel whose waves hold 32 rows each (mx_attn_rows.hpp): rows of its
 // tiles, workgroups per compute unit.
 int attn_rows_tile(int D);
 int attn_rows_per_cu(int D);
 void launch_attn_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);
+void launch_attn_rows_wide(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);  // D > 128 (mx_attn_rows_wide.hip)
 
 }  // namespace mx

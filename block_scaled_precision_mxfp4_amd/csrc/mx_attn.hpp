@@ -207,30 +207,28 @@ struct AttnLds {
 
     // LDS addresses of this lane's K fragments of a block (bf16: product s,
     // columns 16 s + 8 (lane / 32) + 0..7; 8 bits: products 2 p and 2 p + 1,
-    // columns 16 (2 p + lane / 32) + 0..7 and + 8..15)
+    // columns 16 (2 p + lane / 32) + 0..7 and + 8..15): fragment s is at the
+    // first one's address, its bits from 32 on changed by s
     static constexpr int KF = FP8 ? NS / 2 : NS;
-    static __device__ __forceinline__ void k_addr(uint32_t base, int lane, uint32_t (&ka)[KF])
+    static __device__ __forceinline__ uint32_t k_first(uint32_t base, int lane)
     {
         const int r = lane & 31, h = lane >> 5;
-#pragma unroll
-        for (int s = 0; s < KF; ++s)
-            ka[s] = base + r * ROWB + ((2 * s + h) ^ kswz(r)) * 16;
+        return base + r * ROWB + (h ^ kswz(r)) * 16;
     }
-    // ... and of its V^T fragments, by block of 32 columns
-    static __device__ __forceinline__ void v_addr(uint32_t base, int lane, uint32_t (&va)[ND])
+    static __device__ __forceinline__ uint32_t k_at(uint32_t first, int s) { return first ^ (uint32_t)(s * 32); }
+    // ... and of its V^T fragments, likewise by block of 32 columns
+    static __device__ __forceinline__ uint32_t v_first(uint32_t base, int lane)
     {
         const int h = lane >> 5, grp = (lane >> 4) & 1, q = lane & 15;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            if constexpr (FP8) {
-                const int i = q >> 1, r = (i >> 2) * 8 + 4 * h + (i & 3);
-                va[d] = base + r * ROWB + (d ^ vswz(r)) * 32 + grp * 16 + (q & 1) * 8;
-            } else {
-                const int r = 4 * h + (q >> 2);
-                va[d] = base + r * ROWB + (d ^ vswz(r)) * 64 + grp * 32 + (q & 3) * 8;
-            }
+        if constexpr (FP8) {
+            const int i = q >> 1, r = (i >> 2) * 8 + 4 * h + (i & 3);
+            return base + r * ROWB + vswz(r) * 32 + grp * 16 + (q & 1) * 8;
+        } else {
+            const int r = 4 * h + (q >> 2);
+            return base + r * ROWB + vswz(r) * 64 + grp * 32 + (q & 3) * 8;
         }
     }
+    static __device__ __forceinline__ uint32_t v_at(uint32_t first, int d) { return first ^ (uint32_t)(d * (FP8 ? 32 : 64)); }
     // columns of this lane's Q fragment s
     static __device__ __forceinline__ int q_col(int s, int lane)
     {
@@ -253,33 +251,56 @@ __device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, const uint8_t 
     return {make_rsrc_u(k + at, bytes), make_rsrc_u(v + at, bytes)};
 }
 
-// A sequence's page table, 64 entries at a time in a register (an entry per
-// lane) and the next 64 on their way: a scalar load per block would be waited
-// for together with the LDS reads behind it.
+// A sequence's page table, 64 entries at a time in LDS (128 of a wave's own: the
+// next 64 are on their way).  Loads into registers would be waited for with every
+// load behind them still in flight; a scalar load is waited for with the LDS
+// reads behind it.
 struct AttnPages {
-    const int32_t *table;
-    int first, last;  // entry of lane 0; the table's last one
-    int ids, next;
-    __device__ __forceinline__ int load(int at, int lane) const { return table[min(at + lane, last)]; }
-    __device__ __forceinline__ void open(const CacheArgs &c, int s, int at, int lane)
+    static constexpr int LDS = 512;  // bytes
+    __amdgpu_buffer_rsrc_t table;
+    uint8_t *lds;
+    int base, first;     // entry at lds[0]; first entry of the present 64
+    uint32_t id[2];      // entries asked for
+    __device__ __forceinline__ void load(int at, int lane)
     {
-        table = c.pages + (int64_t)s * c.ld_pages;
-        last = c.max_pages - 1;
-        first = at;
-        ids = load(at, lane);
-        next = load(at + 64, lane);
+        load4_to_lds(table, (lds_void *)(lds + ((at - base) & 64) * 4), (uint32_t)(at + lane) * 4);
     }
-    // at: wave-uniform, from one call to the next by less than 64 upwards
-    __device__ __forceinline__ int page(int at, int lane)
+    // (waits for every load of the wave); at: wave-uniform
+    __device__ __forceinline__ void open(const CacheArgs &c, int s, int at, uint8_t *mine, int lane)
     {
-        if (at >= first + 64) {
+        table = make_rsrc_u(c.pages + (int64_t)s * c.ld_pages, (uint32_t)c.max_pages * 4);  // (behind it: page 0)
+        lds = mine;
+        base = first = at;
+        load(at, lane);
+        load(at + 64, lane);
+        attn_wait_vm<0>();
+    }
+    // Ask for entries a and b >= a (both less than 64 behind the ones asked for
+    // before); take them later
+    __device__ __forceinline__ void ask(int a, int b, int lane)
+    {
+        if (a >= first + 64) {
             first += 64;
-            ids = next;
-            next = load(first + 64, lane);
+            load(first + 64, lane);
         }
-        return __builtin_amdgcn_readlane(ids, at - first);
+        id[0] = lds_read4<0>(lds_addr(lds) + ((a - base) & 127) * 4);
+        id[1] = lds_read4<0>(lds_addr(lds) + ((b - base) & 127) * 4);
+    }
+    __device__ __forceinline__ void take(int &a, int &b)
+    {
+        lds_wait_n<0>(id);
+        a = __builtin_amdgcn_readfirstlane((int)id[0]);
+        b = __builtin_amdgcn_readfirstlane((int)id[1]);
     }
 };
+
+// x, as a value that is new here: what is computed from it is not moved out of
+// the loop over units (the addresses of a unit's end, 70 registers, would be).
+__device__ __forceinline__ int anew(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // The kernel's arguments read again: fields that only the end of a unit needs
 // would else be kept in scalar registers over its loop (100 of them spilled).
@@ -322,7 +343,7 @@ __device__ __forceinline__ void negate_q(v4i (&q)[NS], bool negate)
 
 // S^T of one block of 32 keys in LDS, for NT tiles of 32 rows
 template <int DP, bool FP8, int NT>
-__device__ __forceinline__ void scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF], uint32_t at, const v4i (&q)[NT][DP / 16],
+__device__ __forceinline__ void scores(uint32_t ka, const v4i (&q)[NT][DP / 16],
                                        v16f (&s)[NT])
 {
     using L = AttnLds<DP, FP8>;
@@ -334,7 +355,7 @@ __device__ __forceinline__ void scores(const uint32_t (&ka)[AttnLds<DP, FP8>::KF
         v4i f[B];
 #pragma unroll
         for (int i = 0; i < B; ++i)
-            f[i] = lds_read16<0>(ka[bc.value * B + i] + at);
+            f[i] = lds_read16<0>(L::k_at(ka, bc.value * B + i));
         static_for<B / 2>([&](auto ic) {
             constexpr int I = 2 * ic.value;
             lds_wait_n<B - I - 2>(f[I], f[I + 1]);
@@ -374,17 +395,11 @@ struct AttnState {
     }
 };
 
-// Scores of NB blocks to P (bf16 pairs, the second product's operands for its
-// two steps of 16 keys a block), raising the maximum where it has to be.
-template <int ND, int NB>
-__device__ __forceinline__ void softmax_blocks(AttnState<ND> &t, const v16f (&s)[NB], float c, v4i (&p)[NB][2])
+// The running maximum raised to x (the scores' maximum over this lane's keys)
+// where it has to be
+template <int ND>
+__device__ __forceinline__ void raise_to(AttnState<ND> &t, float x, float c)
 {
-    float x = s[0][0];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int g = 0; g < 16; ++g)
-            x = fmaxf(x, s[b][g]);
     x = row_max(x) * c;
     if (__builtin_amdgcn_ballot_w64(x > t.m + kRaise)) {
         const float m = fmaxf(t.m, x);
@@ -397,23 +412,40 @@ __device__ __forceinline__ void softmax_blocks(AttnState<ND> &t, const v16f (&s)
             for (int g = 0; g < 16; ++g)
                 t.o[d][g] *= w;
     }
-    // a row that has seen no key yet: every score is -inf, p = 0
-    const float m = t.m == kNegInf ? 0.0f : t.m;
+}
+template <int ND>
+__device__ __forceinline__ void raise_max(AttnState<ND> &t, const v16f &s, float c)
+{
+    float x = s[0];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        float e[16];
+    for (int g = 1; g < 16; ++g)
+        x = fmaxf(x, s[g]);
+    raise_to(t, x, c);
+}
+
+// What p = 2^(c s - m) subtracts; a row that has seen no key yet: every score
+// is -inf, p = 0
+__device__ __forceinline__ float less_max(float m) { return m == kNegInf ? 0.0f : -m; }
+
+// Scores 2 i and 2 i + 1 of a block to P (bf16 pairs, the second product's
+// operands for its two steps of 16 keys), and to the sum.  (The results stay
+// where they are written: the compiler would put them off until P is needed.)
+template <int ND>
+__device__ __forceinline__ void exponential_pair(AttnState<ND> &t, const v16f &s, int i, float c, float less, v4i (&p)[2])
+{
+    const float e0 = exp2_fast(fmaf(s[2 * i], c, less)), e1 = exp2_fast(fmaf(s[2 * i + 1], c, less));
+    int w = (int)bf16x2_rne(e0, e1);
+    t.l += e0 + e1;
+    asm volatile("" : "+v"(w), "+v"(t.l));
+    p[i >> 2][i & 3] = w;
+}
+template <int ND>
+__device__ __forceinline__ void exponentials(AttnState<ND> &t, const v16f &s, float c, v4i (&p)[2])
+{
+    const float less = less_max(t.m);
 #pragma unroll
-        for (int g = 0; g < 16; ++g)
-            e[g] = exp2_fast(fmaf(s[b][g], c, -m));
-        float sum[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            sum[i] = (e[4 * i] + e[4 * i + 1]) + (e[4 * i + 2] + e[4 * i + 3]);
-        t.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            p[b][i >> 2][i & 3] = (int)bf16x2_rne(e[2 * i], e[2 * i + 1]);
-    }
+    for (int i = 0; i < 8; ++i)
+        exponential_pair(t, s, i, c, less, p);
 }
 
 // V^T fragments of columns 32 d .. 32 d + 31, keys' step s (16 keys)
@@ -450,9 +482,8 @@ __device__ __forceinline__ bool special_pair(int w)
 // The products with V^T where it holds infinities or NaN and some rows do not
 // see all keys: key by key, added to the rows that see it (0 times an infinity
 // is a NaN: a p of 0 does not keep it out).
-__device__ __forceinline__ v16f values_apart(const v4i (&w)[2], const v4i (&p)[2], int lo, int hi, int lane)
+__device__ __forceinline__ void values_apart(const v4i (&w)[2], const v4i (&p)[2], int lo, int hi, int lane, v16f &o)
 {
-    v16f sum = {};
 #pragma unroll 1
     for (int key = 0; key < 32; ++key) {
         // the key's slot: step key / 16, lane half (key / 4) % 2, element 4 ((key / 8) % 2) + key % 4
@@ -469,16 +500,15 @@ __device__ __forceinline__ v16f values_apart(const v4i (&w)[2], const v4i (&p)[2
         const bool sees = key >= lo && key < hi;
 #pragma unroll
         for (int g = 0; g < 16; ++g)
-            sum[g] += sees ? x[g] : 0.0f;
+            o[g] += sees ? x[g] : 0.0f;
     }
-    return sum;
 }
 
 // O^T += V^T P^T of one block, for NT tiles of 32 rows.  masked (wave-uniform):
 // some rows do not see some of its keys; lo, hi: keys of the block that this
 // lane's row of a tile sees.
 template <int DP, bool FP8, int NT>
-__device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND], uint32_t at, const v4i (&p)[NT][2],
+__device__ __forceinline__ void values(uint32_t va, const v4i (&p)[NT][2],
                                        AttnState<AttnLds<DP, FP8>::ND> (&t)[NT], bool masked, const int (&lo)[NT],
                                        const int (&hi)[NT], int lane)
 {
@@ -490,8 +520,8 @@ __device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND
         V f[B][2];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-            f[i][0].template read<0>(va[D0 + i] + at);
-            f[i][1].template read<1>(va[D0 + i] + at);
+            f[i][0].template read<0>(L::v_at(va, D0 + i));
+            f[i][1].template read<1>(L::v_at(va, D0 + i));
         }
         static_for<B>([&](auto ic) {
             constexpr int I = ic.value;
@@ -504,12 +534,8 @@ __device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND
                     special |= special_pair(w[e >> 2][e & 3]);
                 if (__builtin_amdgcn_ballot_w64(special)) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const v16f x = values_apart(w, p[n], lo[n], hi[n], lane);
-#pragma unroll
-                        for (int g = 0; g < 16; ++g)
-                            t[n].o[D0 + I][g] += x[g];
-                    }
+                    for (int n = 0; n < NT; ++n)
+                        values_apart(w, p[n], lo[n], hi[n], lane, t[n].o[D0 + I]);
                     w[0] = w[1] = v4i{0, 0, 0, 0};
                 }
             }
@@ -522,15 +548,87 @@ __device__ __forceinline__ void values(const uint32_t (&va)[AttnLds<DP, FP8>::ND
     });
 }
 
+// Both products for one tile of 32 rows and one block of keys, in groups of two
+// matrix instructions (64 cycles).  A group's fragments are read some groups
+// before it (an LDS read takes 130 cycles and more with eight waves reading),
+// and behind each group stands a piece of other work, fill(group): a wave issues
+// one instruction in 4 cycles, so what is put there costs nothing while the
+// matrix unit works.
+constexpr int kAheadK = 2, kAheadV = 2;
+
+template <int DP, typename F>
+__device__ __forceinline__ v16f scores_filled(uint32_t ka, const v4i (&q)[DP / 16], F &&fill)
+{
+    using L = AttnLds<DP, false>;
+    constexpr int N = L::NS / 2;  // groups: two steps over d
+    v4i f[kAheadK + 1][2];
+    auto read = [&](auto gc) __attribute__((always_inline)) {
+        constexpr int G = gc.value;
+        if constexpr (G < N)
+            static_for<2>([&](auto ic) { f[G % (kAheadK + 1)][ic.value] = lds_read16<0>(L::k_at(ka, 2 * G + ic.value)); });
+    };
+    v16f acc = {};
+    static_for<kAheadK>([&](auto gc) { read(gc); });
+    static_for<N>([&](auto gc) {
+        constexpr int G = gc.value;
+        read(std::integral_constant<int, G + kAheadK>{});
+        constexpr int LATER = N - 1 - G < kAheadK ? N - 1 - G : kAheadK;  // groups read and not multiplied yet
+        lds_wait_n<2 * LATER>(f[G % (kAheadK + 1)]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            acc = mfma32(f[G % (kAheadK + 1)][i], q[2 * G + i], acc);
+        fill(gc);
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    return acc;
+}
+template <int DP>
+constexpr int kScoreGroups = AttnLds<DP, false>::NS / 2;
+
+template <int DP, typename F>
+__device__ __forceinline__ void values_filled(uint32_t va, const v4i (&p)[2], AttnState<AttnLds<DP, false>::ND> &t, F &&fill)
+{
+    using L = AttnLds<DP, false>;
+    constexpr int C = 2;                    // blocks of columns of a group
+    constexpr int N = 2 * (L::ND / C);      // groups: steps of 16 keys, pairs of blocks of columns
+    v2u f[kAheadV + 1][C][2];
+    auto read = [&](auto nc) __attribute__((always_inline)) {
+        if constexpr (nc.value < N) {
+            constexpr int S = nc.value / (L::ND / C), D0 = nc.value % (L::ND / C) * C;
+#pragma unroll
+            for (int d = 0; d < C; ++d) {
+                f[nc.value % (kAheadV + 1)][d][0] = lds_read_tr16<S * 16 * L::ROWB>(L::v_at(va, D0 + d));
+                f[nc.value % (kAheadV + 1)][d][1] = lds_read_tr16<(S * 16 + 8) * L::ROWB>(L::v_at(va, D0 + d));
+            }
+        }
+    };
+    static_for<kAheadV>([&](auto nc) { read(nc); });
+    static_for<N>([&](auto nc) {
+        constexpr int I = nc.value, S = I / (L::ND / C), D0 = I % (L::ND / C) * C;
+        read(std::integral_constant<int, I + kAheadV>{});
+        constexpr int LATER = N - 1 - I < kAheadV ? N - 1 - I : kAheadV;
+        lds_wait_n<2 * C * LATER>(f[I % (kAheadV + 1)]);
+#pragma unroll
+        for (int d = 0; d < C; ++d) {
+            const v2u (&w)[2] = f[I % (kAheadV + 1)][d];
+            t.o[D0 + d] = mfma32(v4i{(int)w[0][0], (int)w[0][1], (int)w[1][0], (int)w[1][1]}, p[S], t.o[D0 + d]);
+        }
+        fill(nc);
+        __builtin_amdgcn_sched_barrier(0);
+    });
+}
+template <int DP>
+constexpr int kValueGroups = AttnLds<DP, false>::ND;
+
 // Scores outside a row's keys to -inf.  lo, hi: relative to the block.
 __device__ __forceinline__ void mask_scores(v16f &s, int lo, int hi, int lane)
 {
     const int h = 4 * (lane >> 5);
+    lo -= h;  // (the limits are moved, not the keys: these stay constants)
+    hi -= h;
 #pragma unroll
-    for (int g = 0; g < 16; ++g) {
-        const int key = 8 * (g >> 2) + h + (g & 3);
-        s[g] = key >= lo && key < hi ? s[g] : kNegInf;
-    }
+    for (int g = 0; g < 16; ++g)
+        s[g] = 8 * (g >> 2) + (g & 3) >= lo && 8 * (g >> 2) + (g & 3) < hi ? s[g] : kNegInf;
 }
 
 // The scale of a key head's scores, as a positive factor (in powers of two),

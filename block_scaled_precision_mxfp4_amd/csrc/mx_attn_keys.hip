@@ -38,17 +38,17 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
     __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
     __shared__ float s_ml[NW][TM][2];
     __shared__ int s_last;
+    __shared__ __attribute__((aligned(16))) uint8_t s_pages[NW][AttnPages::LDS];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg = blockIdx.x;
     const AttnFirst first_loads = attn_first(a, lane);
 
-    uint32_t ko[L::NIH], vo[L::NIH], ka[L::KF], va[L::ND];
+    uint32_t ko[L::NIH], vo[L::NIH];
     L::load_offsets(a.c, lane, ko, vo);
     uint8_t *mine = ring + wave * (ST * STAGE);
-    L::k_addr(lds_addr(mine), lane, ka);
-    L::v_addr(lds_addr(mine) + L::BLOCK, lane, va);
+    const uint32_t ka = L::k_first(lds_addr(mine), lane), va = L::v_first(lds_addr(mine) + L::BLOCK, lane);
 
     AttnPlan plan;
     if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
@@ -82,7 +82,9 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         AttnPages table;
         auto issue = [&](int i) __attribute__((always_inline)) {
             const int key0 = (b0 + wave + i * NW) * 32, len = i < nb ? q.len : 0;
-            const int pg0 = table.page(key0 >> a.c.page_shift, lane), pg1 = table.page((key0 + 16) >> a.c.page_shift, lane);
+            int pg0, pg1;
+            table.take(pg0, pg1);
+            table.ask((key0 + NW * 32) >> a.c.page_shift, (key0 + NW * 32 + 16) >> a.c.page_shift, lane);
             const AttnRows x = attn_rows(a.c, k_head, v_head, pg0, key0, len);
             const AttnRows y = attn_rows(a.c, k_head, v_head, pg1, key0 + 16, len);
             uint8_t *to = mine + (i % ST) * STAGE;
@@ -114,7 +116,9 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             row_lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
         }
         if (nb > 0) {
-            table.open(a.c, s, ((b0 + wave) * 32) >> a.c.page_shift, lane);
+            const int key0 = (b0 + wave) * 32;
+            table.open(a.c, s, key0 >> a.c.page_shift, s_pages[wave], lane);
+            table.ask(key0 >> a.c.page_shift, (key0 + 16) >> a.c.page_shift, lane);
             v4i qf[NT][L::NS];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                 const int key0 = (b0 + wave + i * NW) * 32;
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
                 v16f x[NT];
-                scores<DP, FP8, NT>(ka, slot, qf, x);
+                scores<DP, FP8, NT>(ka + slot, qf, x);
                 const bool masked = key0 < all_lo || key0 + 32 > all_hi;
                 int lo_b[NT], hi_b[NT];
                 v4i p[NT][2];
@@ -145,23 +149,21 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                     hi_b[n] = row_hi[n] - key0;
                     if (masked)
                         mask_scores(x[n], lo_b[n], hi_b[n], lane);
-                    v16f y[1] = {x[n]};
-                    v4i w[1][2];
-                    softmax_blocks(t[n], y, sc.c, w);
-                    p[n][0] = w[0][0];
-                    p[n][1] = w[0][1];
+                    raise_max(t[n], x[n], sc.c);
+                    exponentials(t[n], x[n], sc.c, p[n]);
                 }
                 attn_wait_vm<(ST - 1) * 2 * NI>();
-                values<DP, FP8, NT>(va, slot, p, t, masked, lo_b, hi_b, lane);
+                values<DP, FP8, NT>(va + slot, p, t, masked, lo_b, hi_b, lane);
             }
         }
         // merge the waves: O to the wave's ring, rows of DP floats whose
         // 16-byte chunks are swizzled by the row
         attn_wait_vm<0>();
         const AttnArgs e = args_again();
+        const int end_thread = anew(threadIdx.x), end_lane = end_thread & 63;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = n * 32 + row;
+            const int r = n * 32 + (end_lane & 31);
             t[n].l = row_sum(t[n].l);
             if (r < rows) {
                 float *o = reinterpret_cast<float *>(mine) + r * DP;
@@ -169,11 +171,11 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                 for (int d = 0; d < L::ND; ++d)
 #pragma unroll
                     for (int g = 0; g < 16; g += 4) {
-                        const int ch = d * 8 + (g >> 2) * 2 + (lane >> 5);
+                        const int ch = d * 8 + (g >> 2) * 2 + (end_lane >> 5);
                         *reinterpret_cast<v4f *>(o + ((ch ^ (r & 15)) * 4)) =
                             v4f{t[n].o[d][g], t[n].o[d][g + 1], t[n].o[d][g + 2], t[n].o[d][g + 3]};
                     }
-                if (lane < 32) {
+                if (end_lane < 32) {
                     s_ml[wave][r][0] = t[n].m;
                     s_ml[wave][r][1] = t[n].l;
                 }
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         };
         // what the waves have in LDS, added up: the result, or this workgroup's part of it
         auto merge = [&](bool result) __attribute__((always_inline)) {
-            for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
+            for (int it = end_thread; it < ((rows * QC + 63) & ~63); it += NW * 64) {
                 const int r = it / QC, c8 = it % QC;
                 const bool live = r < rows && c8 * 8 < e.c.D;
                 const int rr = min(r, rows - 1);
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                 };
                 if (parts <= PB) {
                     // few parts: every thread adds up its own pieces of rows
-                    for (int it = threadIdx.x; it < ((rows * QC + 63) & ~63); it += NW * 64) {
+                    for (int it = end_thread; it < ((rows * QC + 63) & ~63); it += NW * 64) {
                         const int r = min(it / QC, rows - 1), c8 = it % QC;
                         float m = kNegInf, l = 0.0f, o[8] = {};
                         add_parts(r, c8, 0, 1, m, l, o);
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
                     done = false;
                 } else {
                     // each wave adds up every NW-th one, into its ring
-                    for (int it = lane; it < rows * QC; it += 64) {
+                    for (int it = end_lane; it < rows * QC; it += 64) {
                         const int r = it / QC, c8 = it % QC;
                         float m = kNegInf, l = 0.0f, o[8] = {};
                         add_parts(r, c8, wave, NW, m, l, o);

@@ -1,0 +1,295 @@
+// Attention of many rows per key head (chunks, whole prompts): the waves of a
+// workgroup hold 32 rows each and share the keys, 64 (32 for wide heads) at a
+// time, in LDS.  Bound by the matrix units and, beside them, the exponentials.
+#pragma once
+
+#include "mx_attn_plan.hpp"
+
+namespace mx {
+
+template <int DP>
+struct RowsShape {
+    static constexpr int NW = DP == 256 ? 4 : 8;
+    static constexpr int TM = NW * 32;           // rows of a tile
+    static constexpr int KT = DP == 256 ? 32 : 64;  // keys of a stage
+    static constexpr int STAGE = 2 * KT * DP * 2;
+    static constexpr int ST = 4;
+    static constexpr int BYTES = ST * STAGE;
+};
+
+template <int DP, bool FP8>
+__global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(AttnArgs a, int mode)
+{
+    using L = AttnLds<DP, false>;  // in LDS the elements are bf16
+    using SH = RowsShape<DP>;
+    constexpr int NW = SH::NW, TM = SH::TM, KT = SH::KT, ST = SH::ST, STAGE = SH::STAGE;
+    constexpr int NB = KT / 32;
+    constexpr int RW = KT / NW;               // rows of a stage that a wave loads: 8, within 16 keys
+    constexpr int IPW = RW / L::RPI;          // its load instructions, of K and of V
+    constexpr int PPW = RW * DP / 8 / 64;     // 8 bits: its pieces of 8 codes
+    static_assert(RW == 8 && IPW >= 1, "a wave's rows of a stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
+    __shared__ int s_last;
+    __shared__ __attribute__((aligned(16))) uint8_t s_pages[NW][AttnPages::LDS];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wg = blockIdx.x;
+    const AttnFirst first_loads = attn_first(a, lane);
+
+    // this lane's places in the cache's rows and in a stage
+    uint32_t ko[FP8 ? PPW : IPW], vo[FP8 ? PPW : IPW], kw[FP8 ? PPW : 1], vw[FP8 ? PPW : 1];
+    const int half = (wave & 1) * 8;  // its first row among 16 keys
+    if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < PPW; ++i) {
+            const int r = (i * 64 + lane) / (DP / 8), c = lane % (DP / 8);
+            ko[i] = vo[i] = c * 8 < a.c.D ? (uint32_t)((half + r) * a.c.token_b + c * 8) : kOOB;
+            kw[i] = (wave * RW + r) * L::ROWB + L::k_chunk(half + r, c) * 16;
+            vw[i] = KT * L::ROWB + (wave * RW + r) * L::ROWB + L::v_chunk(half + r, c) * 16;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < IPW; ++j) {
+            const int r = half + j * L::RPI + lane / L::CH, c = lane % L::CH;
+            const int kc = L::k_chunk(r, c) * 16, vc = L::v_chunk(r, c) * 16;
+            ko[j] = kc < 2 * a.c.D ? (uint32_t)(r * a.c.token_b + kc) : kOOB;
+            vo[j] = vc < 2 * a.c.D ? (uint32_t)(r * a.c.token_b + vc) : kOOB;
+        }
+    }
+    const uint32_t ka = L::k_first(lds_addr(ring), lane), va = L::v_first(lds_addr(ring) + KT * L::ROWB, lane);
+
+    AttnPlan plan;
+    if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+        return;
+    int at = wg * plan.chunk;
+    const int end = min(at + plan.chunk, plan.total);
+    int s = plan.s, seq_start = plan.start;
+    AttnSeq q = plan.q;
+    int cost = seq_steps(a, q, TM, plan.per), units = seq_units(a, q, TM);
+    while (at < end) {
+        while (at >= seq_start + units * cost) {
+            seq_start += units * cost;
+            if (++s >= a.c.seqs)
+                return;
+            q = load_seq(a.c, a.T, s);
+            cost = seq_steps(a, q, TM, plan.per);
+            units = seq_units(a, q, TM);
+        }
+        const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
+        // the tiles with the most keys first
+        const int nth = quotient(u, a.by_kv_heads), head = u - nth * a.c.kv_heads;
+        const int tile = seq_tiles(q, a.group, TM) - 1 - nth;
+        const int piece_end = min(end, unit_start + cost);
+        const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
+        int lo, hi;
+        tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
+        const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
+        const int k0 = max(keys.lo, lo / KT * KT), k1 = keys.hi;
+        const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
+
+        const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
+        const int my_key = k0 + (wave >> 1) * 16;  // the 16 keys that this wave's rows are among
+        AttnPages table;
+        if (nt > 0) {
+            table.open(a.c, s, my_key >> a.c.page_shift, s_pages[wave], lane);
+            table.ask(my_key >> a.c.page_shift, my_key >> a.c.page_shift, lane);
+        }
+        v2u kr[PPW], vr[PPW];
+        // loads of stage i: into LDS, or (8 bits) into registers
+        auto issue = [&](int i) __attribute__((always_inline)) {
+            const int key = my_key + i * KT;
+            int page, same;
+            table.take(page, same);
+            table.ask((key + KT) >> a.c.page_shift, (key + KT) >> a.c.page_shift, lane);
+            const AttnRows x = attn_rows(a.c, k_head, v_head, page, key, i < nt ? q.len : 0);
+            if constexpr (FP8) {
+#pragma unroll
+                for (int j = 0; j < PPW; ++j) {
+                    kr[j] = load8(x.k, ko[j]);
+                    vr[j] = load8(x.v, vo[j]);
+                }
+            } else {
+                uint8_t *to = ring + (i % ST) * STAGE + wave * RW * L::ROWB;
+#pragma unroll
+                for (int j = 0; j < IPW; ++j) {
+                    load16_to_lds(x.k, (lds_void *)(to + j * 1024), ko[j]);
+                    load16_to_lds(x.v, (lds_void *)(to + KT * L::ROWB + j * 1024), vo[j]);
+                }
+            }
+        };
+        auto put = [&](int i) __attribute__((always_inline)) {
+            if constexpr (FP8) {
+                uint8_t *to = ring + (i % ST) * STAGE;
+#pragma unroll
+                for (int j = 0; j < PPW; ++j) {
+                    *reinterpret_cast<v4i *>(to + kw[j]) = bf16_of_fp8(kr[j]);
+                    *reinterpret_cast<v4i *>(to + vw[j]) = bf16_of_fp8(vr[j]);
+                }
+            }
+        };
+
+        AttnState<L::ND> ts[1];
+        AttnState<L::ND> &t = ts[0];
+        t.reset();
+        const AttnScale sc = attn_scale(a, head);
+        const int w0 = r0 + wave * 32, wrows = min(max(rows - wave * 32, 0), 32);  // this wave's rows
+        const int row = lane & 31;
+        const int rr = w0 + min(row, max(wrows - 1, 0));
+        const AttnRow my = attn_row(a, rr, head);
+        const int idx = my.token, pos = q.len - q.n + idx;
+        const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
+        const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        // keys that every row of the wave sees, and that some see
+        const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 31) : 0;
+        const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
+        const int any_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 0) : 0;
+        const int any_hi = wrows > 0 ? __builtin_amdgcn_readlane(row_hi, 31) : 0;
+        v4i qf[L::NS];
+        load_q<DP, false>(a, a.Q + (int64_t)(q.t0 + idx) * a.ldq + my.head * a.c.D,
+                          row < wrows && !sc.zero, lane, qf);
+        negate_q(qf, sc.negate);
+        // Blocks of 32 keys, counted from k0: [s0, s1) are seen by some row of the
+        // wave, [f0, f1) by all of them
+        const int blocks = nt * NB;
+        const int s0 = max(any_lo - k0, 0) / 32, s1 = min((any_hi - k0 + 31) >> 5, blocks);
+        const int f0 = (max(all_lo - k0, 0) + 31) / 32, f1 = min((all_hi - k0) >> 5, s1);
+        v16f x;  // scores of the block whose exponentials are next
+        auto slot = [&](int c) { return (uint32_t)((c / NB % ST) * STAGE + c % NB * L::BLOCK); };
+        if (nt > 0) {
+            constexpr int AHEAD = ST - 2;
+            // stage i is there, and everyone is done with stage i - 2
+            auto sync = [&] __attribute__((always_inline)) {
+                if constexpr (FP8)
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                else
+                    stage_sync<(AHEAD - 1) * 2 * IPW>();
+            };
+            auto load_ahead = [&](int i) __attribute__((always_inline)) {
+                if constexpr (FP8) {
+                    put(i + 1);
+                    issue(i + 2);
+                } else {
+                    issue(i + AHEAD);
+                }
+            };
+            // the scores of block c beside the exponentials of block c - 1, then the
+            // latter's values beside the maximum of the former
+            auto step = [&](int i, auto bc) __attribute__((always_inline)) {
+                const int c = i * NB + bc.value;
+                const float less = less_max(t.m);
+                constexpr int PAIRS = 8, G1 = kScoreGroups<DP>, EACH = (PAIRS + G1 - 2) / (G1 - 1);  // (all but the last group)
+                v4i p[2];
+                x = scores_filled<DP>(ka + slot(c), qf, [&](auto gc) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int n = gc.value * EACH; n < (gc.value + 1) * EACH && n < PAIRS; ++n)
+                        exponential_pair(t, x, n, sc.c, less, p);
+                });
+                constexpr int G2 = kValueGroups<DP>, MAX = 16 / G2;
+                float most = kNegInf;
+                values_filled<DP>(va + slot(c - 1), p, t, [&](auto gc) __attribute__((always_inline)) {
+                    if constexpr (gc.value == 0 && bc.value == 0)
+                        load_ahead(i);
+#pragma unroll
+                    for (int n = gc.value * MAX; n < (gc.value + 1) * MAX; ++n)
+                        most = fmaxf(most, x[n]);
+                });
+                raise_to(t, most, sc.c);
+            };
+            if constexpr (FP8) {
+                issue(0);
+                put(0);
+                issue(1);
+            } else {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    issue(i);
+            }
+            const int hot0 = f0 / NB + 1, hot1 = f1 / NB;  // stages whose blocks, and the one before, are seen by all rows
+            for (int i = 0; i <= nt; ++i) {
+                for (; i >= hot0 && i < hot1; ++i) {
+                    sync();
+                    static_for<NB>([&](auto bc) { step(i, bc); });
+                }
+                sync();
+                load_ahead(i);
+#pragma unroll 1
+                for (int c = i * NB; c < (i + 1) * NB; ++c) {
+                    if (c - 1 >= s0 && c - 1 < s1) {
+                        v4i p[1][2];
+                        exponentials(t, x, sc.c, p[0]);
+                        const int lo_c[1] = {row_lo - (k0 + (c - 1) * 32)}, hi_c[1] = {row_hi - (k0 + (c - 1) * 32)};
+                        values<DP, false, 1>(va + slot(c - 1), p, ts, c - 1 < f0 || c - 1 >= f1, lo_c, hi_c, lane);
+                    }
+                    if (c >= s0 && c < s1) {
+                        x = scores_filled<DP>(ka + slot(c), qf, [](auto) {});
+                        if (c < f0 || c >= f1)
+                            mask_scores(x, row_lo - (k0 + c * 32), row_hi - (k0 + c * 32), lane);
+                        raise_max(t, x, sc.c);
+                    }
+                }
+            }
+        }
+        attn_wait_vm<0>();
+        const AttnArgs end_args = args_again();
+        const int end_lane = anew(lane);
+        t.l = row_sum(t.l);
+        __syncthreads();  // the ring is free
+        const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
+        bool done = first == last;
+        if (!done) {
+            // a partial result: a wave's registers as they are
+            constexpr int64_t PW = 64 * (L::ND * 16 + 2);  // floats of a wave
+            const __amdgpu_buffer_rsrc_t to =
+                make_rsrc_u(end_args.partials + (2 * (int64_t)wg + (unit_start > wg * plan.chunk ? 1 : 0)) * (NW * PW) + wave * PW, PW * 4);
+            if (wrows > 0) {
+#pragma unroll
+                for (int d = 0; d < L::ND; ++d)
+#pragma unroll
+                    for (int g = 0; g < 16; g += 4)
+                        store16_coherent(to, (uint32_t)(((d * 4 + (g >> 2)) * 64 + end_lane) * 16),
+                                         v4f{t.o[d][g], t.o[d][g + 1], t.o[d][g + 2], t.o[d][g + 3]});
+                __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(t.m), __float_as_uint(t.l)}, to,
+                                                      (uint32_t)(L::ND * 16 * 256 + end_lane * 8), 0, kCoherent);
+            }
+            done = split_arrive_last_via(end_args.counters + first, last - first + 1, &s_last);
+            if (done && wrows > 0) {
+                const int off = unit_start > first * plan.chunk ? 1 : 0;
+                t.reset();
+                for (int w = 0; w <= last - first; ++w) {
+                    const __amdgpu_buffer_rsrc_t from = make_rsrc_u(
+                        end_args.partials + (2 * (int64_t)(first + w) + (w == 0 ? off : 0)) * (NW * PW) + wave * PW, PW * 4);
+                    const v2u ml = __builtin_amdgcn_raw_buffer_load_b64(from, (uint32_t)(L::ND * 16 * 256 + end_lane * 8), 0, kCoherent);
+                    const float mw = __uint_as_float(ml[0]), n = fmaxf(t.m, mw);
+                    const float f0 = n == kNegInf ? 1.0f : exp2_fast(t.m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
+                    t.m = n;
+                    t.l = t.l * f0 + __uint_as_float(ml[1]) * f1;
+#pragma unroll
+                    for (int d = 0; d < L::ND; ++d)
+#pragma unroll
+                        for (int g = 0; g < 16; g += 4) {
+                            const v4f x = load16_coherent(from, (uint32_t)(((d * 4 + (g >> 2)) * 64 + end_lane) * 16));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                t.o[d][g + e] = t.o[d][g + e] * f0 + x[e] * f1;
+                        }
+                }
+            }
+        }
+        if (done && wrows > 0)
+            finish_tile<DP>(end_args, q, head, w0, wrows, t.m, t.l, t.o, ring + wave * (32 * DP * 2), end_lane);
+        __syncthreads();  // the ring is free again
+        at = piece_end;
+    }
+}
+
+template <int DP>
+void launch_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
+{
+    if (fp8)
+        mx_attn_rows_kernel<DP, true><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
+    else
+        mx_attn_rows_kernel<DP, false><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
+}
+
+}  // namespace mx

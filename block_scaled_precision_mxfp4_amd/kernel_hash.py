@@ -20,7 +20,8 @@ FAMILY_FILES = {
     "stream": _COMMON + ("mx_stream.hip",),
     "experts": _COMMON + ("mx_experts.hpp", "mx_route.hip", "mx_group.hpp", "mx_grouped.hip", "mx_tile_grouped.hip", "mx_glu.hip",
                           "mx_norm.hip", "mx_quantize.hpp", "mx_quantize_out.hpp", "mx_rows16.hpp"),
-    "attention": _COMMON + ("mx_attention.hpp", "mx_append.hip", "mx_attn.hpp", "mx_attn_plan.hpp", "mx_attn_keys.hip",
+    "attention": _COMMON + ("mx_attention.hpp", "mx_append.hip", "mx_attn.hpp", "mx_attn_plan.hpp", "mx_attn_keys.hip", "mx_attn_rows.hpp",
+                            "mx_attn_rows.hip", "mx_attn_rows_wide.hip",
                             "mx_quantize.hpp", "mx_quantize_out.hpp", "mx_rows16.hpp"),
 }
 
