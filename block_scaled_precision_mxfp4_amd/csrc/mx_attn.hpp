@@ -260,7 +260,6 @@ struct AttnPages {
     __amdgpu_buffer_rsrc_t table;
     uint8_t *lds;
     int base, first;     // entry at lds[0]; first entry of the present 64
-    uint32_t id[2];      // entries asked for
     __device__ __forceinline__ void load(int at, int lane)
     {
         load4_to_lds(table, (lds_void *)(lds + ((at - base) & 64) * 4), (uint32_t)(at + lane) * 4);
@@ -275,22 +274,22 @@ struct AttnPages {
         load(at + 64, lane);
         attn_wait_vm<0>();
     }
-    // Ask for entries a and b >= a (both less than 64 behind the ones asked for
-    // before); take them later
-    __device__ __forceinline__ void ask(int a, int b, int lane)
+    // Entries a and b >= a (both less than 64 behind the ones before); the read and
+    // its wait are one piece, so that no value in flight is ever in a register
+    __device__ __forceinline__ void get(int a, int b, int lane, int &page_a, int &page_b)
     {
         if (a >= first + 64) {
             first += 64;
             load(first + 64, lane);
         }
-        id[0] = lds_read4<0>(lds_addr(lds) + ((a - base) & 127) * 4);
-        id[1] = lds_read4<0>(lds_addr(lds) + ((b - base) & 127) * 4);
-    }
-    __device__ __forceinline__ void take(int &a, int &b)
-    {
-        lds_wait_n<0>(id);
-        a = __builtin_amdgcn_readfirstlane((int)id[0]);
-        b = __builtin_amdgcn_readfirstlane((int)id[1]);
+        const uint32_t at = lds_addr(lds), x = at + ((a - base) & 127) * 4, y = at + ((b - base) & 127) * 4;
+        uint32_t r, s;
+        asm volatile("ds_read_b32 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(r), "=&v"(s)
+                     : "v"(x), "v"(y)
+                     : "memory");
+        page_a = __builtin_amdgcn_readfirstlane((int)r);
+        page_b = __builtin_amdgcn_readfirstlane((int)s);
     }
 };
 
@@ -548,77 +547,14 @@ __device__ __forceinline__ void values(uint32_t va, const v4i (&p)[NT][2],
     });
 }
 
-// Both products for one tile of 32 rows and one block of keys, in groups of two
-// matrix instructions (64 cycles).  A group's fragments are read some groups
-// before it (an LDS read takes 130 cycles and more with eight waves reading),
-// and behind each group stands a piece of other work, fill(group): a wave issues
-// one instruction in 4 cycles, so what is put there costs nothing while the
-// matrix unit works.
-constexpr int kAheadK = 2, kAheadV = 2;
-
-template <int DP, typename F>
-__device__ __forceinline__ v16f scores_filled(uint32_t ka, const v4i (&q)[DP / 16], F &&fill)
-{
-    using L = AttnLds<DP, false>;
-    constexpr int N = L::NS / 2;  // groups: two steps over d
-    v4i f[kAheadK + 1][2];
-    auto read = [&](auto gc) __attribute__((always_inline)) {
-        constexpr int G = gc.value;
-        if constexpr (G < N)
-            static_for<2>([&](auto ic) { f[G % (kAheadK + 1)][ic.value] = lds_read16<0>(L::k_at(ka, 2 * G + ic.value)); });
-    };
-    v16f acc = {};
-    static_for<kAheadK>([&](auto gc) { read(gc); });
-    static_for<N>([&](auto gc) {
-        constexpr int G = gc.value;
-        read(std::integral_constant<int, G + kAheadK>{});
-        constexpr int LATER = N - 1 - G < kAheadK ? N - 1 - G : kAheadK;  // groups read and not multiplied yet
-        lds_wait_n<2 * LATER>(f[G % (kAheadK + 1)]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            acc = mfma32(f[G % (kAheadK + 1)][i], q[2 * G + i], acc);
-        fill(gc);
-        __builtin_amdgcn_sched_barrier(0);
-    });
-    return acc;
-}
+// The scores of one block for one tile of 32 rows
 template <int DP>
-constexpr int kScoreGroups = AttnLds<DP, false>::NS / 2;
-
-template <int DP, typename F>
-__device__ __forceinline__ void values_filled(uint32_t va, const v4i (&p)[2], AttnState<AttnLds<DP, false>::ND> &t, F &&fill)
+__device__ __forceinline__ v16f scores_one(uint32_t ka, const v4i (&q)[DP / 16])
 {
-    using L = AttnLds<DP, false>;
-    constexpr int C = 2;                    // blocks of columns of a group
-    constexpr int N = 2 * (L::ND / C);      // groups: steps of 16 keys, pairs of blocks of columns
-    v2u f[kAheadV + 1][C][2];
-    auto read = [&](auto nc) __attribute__((always_inline)) {
-        if constexpr (nc.value < N) {
-            constexpr int S = nc.value / (L::ND / C), D0 = nc.value % (L::ND / C) * C;
-#pragma unroll
-            for (int d = 0; d < C; ++d) {
-                f[nc.value % (kAheadV + 1)][d][0] = lds_read_tr16<S * 16 * L::ROWB>(L::v_at(va, D0 + d));
-                f[nc.value % (kAheadV + 1)][d][1] = lds_read_tr16<(S * 16 + 8) * L::ROWB>(L::v_at(va, D0 + d));
-            }
-        }
-    };
-    static_for<kAheadV>([&](auto nc) { read(nc); });
-    static_for<N>([&](auto nc) {
-        constexpr int I = nc.value, S = I / (L::ND / C), D0 = I % (L::ND / C) * C;
-        read(std::integral_constant<int, I + kAheadV>{});
-        constexpr int LATER = N - 1 - I < kAheadV ? N - 1 - I : kAheadV;
-        lds_wait_n<2 * C * LATER>(f[I % (kAheadV + 1)]);
-#pragma unroll
-        for (int d = 0; d < C; ++d) {
-            const v2u (&w)[2] = f[I % (kAheadV + 1)][d];
-            t.o[D0 + d] = mfma32(v4i{(int)w[0][0], (int)w[0][1], (int)w[1][0], (int)w[1][1]}, p[S], t.o[D0 + d]);
-        }
-        fill(nc);
-        __builtin_amdgcn_sched_barrier(0);
-    });
+    v16f s[1];
+    scores<DP, false, 1>(ka, reinterpret_cast<const v4i (&)[1][DP / 16]>(q), s);
+    return s[0];
 }
-template <int DP>
-constexpr int kValueGroups = AttnLds<DP, false>::ND;
 
 // Scores outside a row's keys to -inf.  lo, hi: relative to the block.
 __device__ __forceinline__ void mask_scores(v16f &s, int lo, int hi, int lane)

@@ -83,8 +83,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
         auto issue = [&](int i) __attribute__((always_inline)) {
             const int key0 = (b0 + wave + i * NW) * 32, len = i < nb ? q.len : 0;
             int pg0, pg1;
-            table.take(pg0, pg1);
-            table.ask((key0 + NW * 32) >> a.c.page_shift, (key0 + NW * 32 + 16) >> a.c.page_shift, lane);
+            table.get(key0 >> a.c.page_shift, (key0 + 16) >> a.c.page_shift, lane, pg0, pg1);
             const AttnRows x = attn_rows(a.c, k_head, v_head, pg0, key0, len);
             const AttnRows y = attn_rows(a.c, k_head, v_head, pg1, key0 + 16, len);
             uint8_t *to = mine + (i % ST) * STAGE;
@@ -116,9 +115,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
             row_lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
         }
         if (nb > 0) {
-            const int key0 = (b0 + wave) * 32;
-            table.open(a.c, s, key0 >> a.c.page_shift, s_pages[wave], lane);
-            table.ask(key0 >> a.c.page_shift, (key0 + 16) >> a.c.page_shift, lane);
+            table.open(a.c, s, ((b0 + wave) * 32) >> a.c.page_shift, s_pages[wave], lane);
             v4i qf[NT][L::NS];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {

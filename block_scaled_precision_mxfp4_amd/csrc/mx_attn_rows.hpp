@@ -91,17 +91,14 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
         const int my_key = k0 + (wave >> 1) * 16;  // the 16 keys that this wave's rows are among
         AttnPages table;
-        if (nt > 0) {
+        if (nt > 0)
             table.open(a.c, s, my_key >> a.c.page_shift, s_pages[wave], lane);
-            table.ask(my_key >> a.c.page_shift, my_key >> a.c.page_shift, lane);
-        }
         v2u kr[PPW], vr[PPW];
         // loads of stage i: into LDS, or (8 bits) into registers
         auto issue = [&](int i) __attribute__((always_inline)) {
             const int key = my_key + i * KT;
             int page, same;
-            table.take(page, same);
-            table.ask((key + KT) >> a.c.page_shift, (key + KT) >> a.c.page_shift, lane);
+            table.get(key >> a.c.page_shift, key >> a.c.page_shift, lane, page, same);
             const AttnRows x = attn_rows(a.c, k_head, v_head, page, key, i < nt ? q.len : 0);
             if constexpr (FP8) {
 #pragma unroll
@@ -158,43 +155,119 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         auto slot = [&](int c) { return (uint32_t)((c / NB % ST) * STAGE + c % NB * L::BLOCK); };
         if (nt > 0) {
             constexpr int AHEAD = ST - 2;
-            // stage i is there, and everyone is done with stage i - 2
+            // Barrier i: stage i is there, and everyone is done with stage i - 2,
+            // whose slot stage i + AHEAD takes.  (Every wave passes every barrier
+            // once; where in its work is its own affair.)
+            int synced = 0;
             auto sync = [&] __attribute__((always_inline)) {
-                if constexpr (FP8)
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                else
-                    stage_sync<(AHEAD - 1) * 2 * IPW>();
-            };
-            auto load_ahead = [&](int i) __attribute__((always_inline)) {
                 if constexpr (FP8) {
-                    put(i + 1);
-                    issue(i + 2);
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    put(synced + 1);
+                    issue(synced + 2);
                 } else {
-                    issue(i + AHEAD);
+                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((AHEAD - 1) * 2 * IPW) : "memory");
+                    issue(synced + AHEAD);
                 }
+                ++synced;
             };
-            // the scores of block c beside the exponentials of block c - 1, then the
-            // latter's values beside the maximum of the former
-            auto step = [&](int i, auto bc) __attribute__((always_inline)) {
-                const int c = i * NB + bc.value;
-                const float less = less_max(t.m);
-                constexpr int PAIRS = 8, G1 = kScoreGroups<DP>, EACH = (PAIRS + G1 - 2) / (G1 - 1);  // (all but the last group)
+            // Stages whose blocks, and the one before, are seen by all rows: for
+            // each block c its scores beside the exponentials of block c - 1, then
+            // that block's values beside the maximum of c.  Both products come in
+            // groups of two matrix instructions (64 cycles); the groups' fragments
+            // are read LA groups before (an LDS read takes 130 cycles and more with
+            // eight waves reading), over the stages' borders too, and behind each
+            // group stands a piece of the other work: a wave issues one instruction
+            // in 4 cycles, so what is put there runs while the matrix unit works.
+            auto hot = [&](int i0, int i1) __attribute__((always_inline)) {
+                constexpr int LA = 3, R = LA + 1;
+                constexpr int NK = L::NS / 2, NV = L::ND, NI = NK + NV;  // groups of a block: scores, values
+                constexpr int T = NB * NI;
+                constexpr bool WRAP = NB > 1;
+                static_assert(T % R == 0, "fragments by group");
+                v4i fk[R][2];
+                v2u fv[R][2][2];
+                auto read = [&](auto nc, int i) __attribute__((always_inline)) {
+                    constexpr int N = nc.value % T, B = N / NI, G = N % NI, F = N % R;
+                    const int c = (i + nc.value / T) * NB + B;
+                    if constexpr (G < NK) {
+                        const uint32_t at = ka + slot(c);
+                        fk[F][0] = lds_read16<0>(L::k_at(at, 2 * G));
+                        fk[F][1] = lds_read16<0>(L::k_at(at, 2 * G + 1));
+                    } else {
+                        constexpr int S = (G - NK) / (L::ND / 2), D0 = (G - NK) % (L::ND / 2) * 2;
+                        const uint32_t at = va + slot(c - 1);
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            fv[F][d][0] = lds_read_tr16<S * 16 * L::ROWB>(L::v_at(at, D0 + d));
+                            fv[F][d][1] = lds_read_tr16<(S * 16 + 8) * L::ROWB>(L::v_at(at, D0 + d));
+                        }
+                    }
+                };
+                // reads of the groups behind group n that are under way with it
+                auto later = [](int n) constexpr {
+                    int r = 0;
+                    for (int k = n + 1; k <= n + LA; ++k)
+                        if (WRAP || k < T)
+                            r += k % T % NI < NK ? 2 : 4;
+                    return r;
+                };
+                auto start = [&](int i) __attribute__((always_inline)) {
+                    static_for<LA>([&](auto nc) { read(nc, i); });
+                };
+                if (synced <= i0)
+                    sync();
+                if constexpr (WRAP)
+                    start(i0);
                 v4i p[2];
-                x = scores_filled<DP>(ka + slot(c), qf, [&](auto gc) __attribute__((always_inline)) {
+                v16f acc;
+                float less, most;
+                for (int i = i0; i < i1; ++i) {
+                    if constexpr (!WRAP) {
+                        if (synced <= i)
+                            sync();
+                        start(i);
+                    }
+                    static_for<T>([&](auto nc) {
+                        constexpr int N = nc.value, B = N / NI, G = N % NI, F = N % R;
+                        if constexpr (WRAP || N + LA < T)
+                            read(std::integral_constant<int, N + LA>{}, i);
+                        if constexpr (G < NK) {
+                            lds_wait_n<later(N)>(fk[F]);
+                            if constexpr (G == 0) {
+                                acc = v16f{};
+                                less = less_max(t.m);
+                            }
+                            acc = mfma32(fk[F][0], qf[2 * G], acc);
+                            acc = mfma32(fk[F][1], qf[2 * G + 1], acc);
+                            constexpr int EACH = (8 + NK - 2) / (NK - 1);  // (pairs; none behind the last group: x is free there)
 #pragma unroll
-                    for (int n = gc.value * EACH; n < (gc.value + 1) * EACH && n < PAIRS; ++n)
-                        exponential_pair(t, x, n, sc.c, less, p);
-                });
-                constexpr int G2 = kValueGroups<DP>, MAX = 16 / G2;
-                float most = kNegInf;
-                values_filled<DP>(va + slot(c - 1), p, t, [&](auto gc) __attribute__((always_inline)) {
-                    if constexpr (gc.value == 0 && bc.value == 0)
-                        load_ahead(i);
+                            for (int n = G * EACH; n < (G + 1) * EACH && n < 8; ++n)
+                                exponential_pair(t, x, n, sc.c, less, p);
+                            if constexpr (G == NK - 1)
+                                x = acc;
+                        } else {
+                            constexpr int I = G - NK, S = I / (L::ND / 2), D0 = I % (L::ND / 2) * 2, MAX = 16 / NV;
+                            lds_wait_n<later(N)>(fv[F]);
 #pragma unroll
-                    for (int n = gc.value * MAX; n < (gc.value + 1) * MAX; ++n)
-                        most = fmaxf(most, x[n]);
-                });
-                raise_to(t, most, sc.c);
+                            for (int d = 0; d < 2; ++d) {
+                                const v2u (&w)[2] = fv[F][d];
+                                t.o[D0 + d] = mfma32(v4i{(int)w[0][0], (int)w[0][1], (int)w[1][0], (int)w[1][1]}, p[S], t.o[D0 + d]);
+                            }
+                            if constexpr (I == 0)
+                                most = x[0];
+#pragma unroll
+                            for (int n = I * MAX; n < (I + 1) * MAX; ++n)
+                                most = fmaxf(most, x[n]);
+                            if constexpr (I == NV - 1)
+                                raise_to(t, most, sc.c);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                        // (the values of stage i - 1 are read: barrier i + 1 may come)
+                        if constexpr (WRAP && N == NI - 1)
+                            sync();
+                    });
+                }
+                lds_wait_n<0>(fk, fv);
             };
             if constexpr (FP8) {
                 issue(0);
@@ -205,14 +278,14 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
                 for (int i = 0; i < AHEAD; ++i)
                     issue(i);
             }
-            const int hot0 = f0 / NB + 1, hot1 = f1 / NB;  // stages whose blocks, and the one before, are seen by all rows
+            const int hot0 = f0 / NB + 1, hot1 = f1 / NB;
             for (int i = 0; i <= nt; ++i) {
-                for (; i >= hot0 && i < hot1; ++i) {
-                    sync();
-                    static_for<NB>([&](auto bc) { step(i, bc); });
+                if (i >= hot0 && i < hot1) {
+                    hot(i, hot1);
+                    i = hot1;
                 }
-                sync();
-                load_ahead(i);
+                if (synced <= i)
+                    sync();
 #pragma unroll 1
                 for (int c = i * NB; c < (i + 1) * NB; ++c) {
                     if (c - 1 >= s0 && c - 1 < s1) {
@@ -222,7 +295,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
                         values<DP, false, 1>(va + slot(c - 1), p, ts, c - 1 < f0 || c - 1 >= f1, lo_c, hi_c, lane);
                     }
                     if (c >= s0 && c < s1) {
-                        x = scores_filled<DP>(ka + slot(c), qf, [](auto) {});
+                        x = scores_one<DP>(ka + slot(c), qf);
                         if (c < f0 || c >= f1)
                             mask_scores(x, row_lo - (k0 + c * 32), row_hi - (k0 + c * 32), lane);
                         raise_max(t, x, sc.c);
