@@ -83,9 +83,12 @@ AttnKeysKernel attn_keys_kernel(int D, bool fp8);
 int64_t attn_partial_floats(int D);
 // The kernel whose waves hold 32 rows each (mx_attn_rows.hpp): rows of its
 // tiles, workgroups per compute unit.
-int attn_rows_tile(int D);
-int attn_rows_per_cu(int D);
-void launch_attn_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);
-void launch_attn_rows_wide(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s);  // D > 128 (mx_attn_rows_wide.hip)
+constexpr int kAttnRowsTile = 256;  // rows of a tile, at most
+struct AttnRowsKernel {
+    int tile, per_cu;
+    AttnLaunchFn launch;
+};
+AttnRowsKernel attn_rows_kernel(int D, bool fp8, bool small);
+AttnRowsKernel attn_rows_kernel_wide(bool fp8);  // D > 128 (mx_attn_rows_wide.hip)
 
 }  // namespace mx

@@ -3,17 +3,13 @@
 
 namespace mx {
 
-int attn_rows_tile(int D) { return D > 128 ? RowsShape<256>::TM : RowsShape<128>::TM; }
-int attn_rows_per_cu(int) { return 1; }
-
-void launch_attn_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
+AttnRowsKernel attn_rows_kernel(int D, bool fp8, bool small)
 {
-    if (a.c.D <= 64)
-        launch_rows<64>(a, fp8, plan, grid, s);
-    else if (a.c.D <= 128)
-        launch_rows<128>(a, fp8, plan, grid, s);
-    else
-        launch_attn_rows_wide(a, fp8, plan, grid, s);
+    if (D <= 64)
+        return small ? rows_entry<64, true>(fp8) : rows_entry<64, false>(fp8);
+    if (D <= 128)
+        return small ? rows_entry<128, true>(fp8) : rows_entry<128, false>(fp8);
+    return attn_rows_kernel_wide(fp8);
 }
 
 }  // namespace mx

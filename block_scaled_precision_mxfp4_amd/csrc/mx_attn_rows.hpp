@@ -7,27 +7,32 @@
 
 namespace mx {
 
-template <int DP>
+// Waves of a workgroup, keys of a stage and stages in LDS.  SMALL: half the rows
+// and two workgroups (of D <= 64 three) on a compute unit, which fill each
+// other's barriers; the large shape reads keys and values half as often.
+// MEASURED
+template <int DP, bool SMALL>
 struct RowsShape {
-    static constexpr int NW = DP == 256 ? 4 : 8;
-    static constexpr int TM = NW * 32;           // rows of a tile
-    static constexpr int KT = DP == 256 ? 32 : 64;  // keys of a stage
+    static constexpr int NW = DP == 256 || SMALL ? 4 : 8;
+    static constexpr int TM = NW * 32;                      // rows of a tile
+    static constexpr int KT = DP == 256 || (SMALL && DP == 128) ? 32 : 64;  // keys of a stage
     static constexpr int STAGE = 2 * KT * DP * 2;
-    static constexpr int ST = 4;
+    static constexpr int ST = SMALL && DP == 64 ? 3 : 4;
     static constexpr int BYTES = ST * STAGE;
+    static constexpr int PER_CU = SMALL && DP < 256 ? 2 : 1;
 };
 
-template <int DP, bool FP8>
-__global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(AttnArgs a, int mode)
+template <int DP, bool FP8, bool SMALL>
+__global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP < 256 ? 2 : 1)) mx_attn_rows_kernel(AttnArgs a, int mode)
 {
     using L = AttnLds<DP, false>;  // in LDS the elements are bf16
-    using SH = RowsShape<DP>;
+    using SH = RowsShape<DP, SMALL>;
     constexpr int NW = SH::NW, TM = SH::TM, KT = SH::KT, ST = SH::ST, STAGE = SH::STAGE;
     constexpr int NB = KT / 32;
-    constexpr int RW = KT / NW;               // rows of a stage that a wave loads: 8, within 16 keys
+    constexpr int RW = KT / NW;               // rows of a stage that a wave loads: 8 or 16, within 16 keys
     constexpr int IPW = RW / L::RPI;          // its load instructions, of K and of V
     constexpr int PPW = RW * DP / 8 / 64;     // 8 bits: its pieces of 8 codes
-    static_assert(RW == 8 && IPW >= 1, "a wave's rows of a stage");
+    static_assert((RW == 8 || RW == 16) && IPW >= 1 && PPW >= 1, "a wave's rows of a stage");
     __shared__ __attribute__((aligned(1024))) uint8_t ring[SH::BYTES];
     __shared__ int s_last;
     __shared__ __attribute__((aligned(16))) uint8_t s_pages[NW][AttnPages::LDS];
@@ -39,7 +44,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
 
     // this lane's places in the cache's rows and in a stage
     uint32_t ko[FP8 ? PPW : IPW], vo[FP8 ? PPW : IPW], kw[FP8 ? PPW : 1], vw[FP8 ? PPW : 1];
-    const int half = (wave & 1) * 8;  // its first row among 16 keys
+    const int half = wave * RW % 16;  // its first row among 16 keys
     if constexpr (FP8) {
 #pragma unroll
         for (int i = 0; i < PPW; ++i) {
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
         const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
 
         const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
-        const int my_key = k0 + (wave >> 1) * 16;  // the 16 keys that this wave's rows are among
+        const int my_key = k0 + wave * RW / 16 * 16;  // the 16 keys that this wave's rows are among
         AttnPages table;
         if (nt > 0)
             table.open(a.c, s, my_key >> a.c.page_shift, s_pages[wave], lane);
@@ -356,13 +361,17 @@ __global__ void __launch_bounds__((RowsShape<DP>::NW * 64)) mx_attn_rows_kernel(
     }
 }
 
-template <int DP>
-void launch_rows(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
+template <int DP, bool SMALL>
+AttnRowsKernel rows_entry(bool fp8)
 {
-    if (fp8)
-        mx_attn_rows_kernel<DP, true><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
-    else
-        mx_attn_rows_kernel<DP, false><<<grid, RowsShape<DP>::NW * 64, 0, s>>>(a, plan);
+    using SH = RowsShape<DP, SMALL>;
+    auto bf16 = [](const AttnArgs &a, int plan, int grid, hipStream_t s) {
+        mx_attn_rows_kernel<DP, false, SMALL><<<grid, SH::NW * 64, 0, s>>>(a, plan);
+    };
+    auto f8 = [](const AttnArgs &a, int plan, int grid, hipStream_t s) {
+        mx_attn_rows_kernel<DP, true, SMALL><<<grid, SH::NW * 64, 0, s>>>(a, plan);
+    };
+    return {SH::TM, SH::PER_CU, fp8 ? (AttnLaunchFn)f8 : (AttnLaunchFn)bf16};
 }
 
 }  // namespace mx

@@ -4,9 +4,6 @@
 
 namespace mx {
 
-void launch_attn_rows_wide(const AttnArgs &a, bool fp8, int plan, int grid, hipStream_t s)
-{
-    launch_rows<256>(a, fp8, plan, grid, s);
-}
+AttnRowsKernel attn_rows_kernel_wide(bool fp8) { return rows_entry<256, false>(fp8); }
 
 }  // namespace mx

@@ -60,6 +60,8 @@ mxgemm_status check_cache(const mxgemm_kv_cache *c, bool pages, mx::CacheArgs &a
     return MXGEMM_OK;
 }
 
+constexpr int64_t kLargeTiles = 256;  // rows (all heads) per compute unit from which the large shape is taken
+
 // Tiles of `tile` rows over all sequences and key heads, at most
 int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
 {
@@ -141,7 +143,7 @@ size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv
 {
     if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
         return 0;
-    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::attn_rows_tile(head_dim) / 32 : 2;
+    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::kAttnRowsTile / 32 : 2;
     return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * parts * mx::attn_partial_floats(head_dim) * 4);
 }
 
@@ -206,12 +208,13 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     const int64_t most_rows = (int64_t)most_new * G;
     const int tile = most_rows <= mx::kAttnTile || !keys.launch[1] ? mx::kAttnTile : 2 * mx::kAttnTile;
     if (most_rows > kKeysRows) {
-        const int64_t tiles = most_units(T, cache->seqs, G, Hk, mx::attn_rows_tile(D));
-        const int64_t wgs = std::min<int64_t>((int64_t)cu * mx::attn_rows_per_cu(D), mx::kAttnPieces);
+        const mx::AttnRowsKernel rows = mx::attn_rows_kernel(D, fp8, (int64_t)Hk * T * G < kLargeTiles * cu);
+        const int64_t tiles = most_units(T, cache->seqs, G, Hk, rows.tile);
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * rows.per_cu, mx::kAttnPieces);
         if (tiles >= 2 * wgs)
-            mx::launch_attn_rows(a, fp8, mx::kPlanWhole, (int)tiles, stream);
+            rows.launch(a, mx::kPlanWhole, (int)tiles, stream);
         else
-            mx::launch_attn_rows(a, fp8, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
+            rows.launch(a, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
     } else {
         const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
         const int64_t wgs = std::min<int64_t>((int64_t)cu * keys.per_cu[tile / mx::kAttnTile - 1], mx::kAttnPieces);
