@@ -83,7 +83,6 @@ AttnKeysKernel attn_keys_kernel(int D, bool fp8);
 int64_t attn_partial_floats(int D);
 // The kernel whose waves hold 32 rows each (mx_attn_rows.hpp): rows of its
 // tiles, workgroups per compute unit.
-constexpr int kAttnRowsTile = 256;  // rows of a tile, at most
 struct AttnRowsKernel {
     int tile, per_cu;
     AttnLaunchFn launch;

@@ -16,20 +16,20 @@ namespace {
 
 // waves of a workgroup and slots of a wave's ring: the most that fit 128 KiB
 // (64 KiB where two workgroups then share a compute unit)
-template <int DP, bool FP8>
+template <int DP, bool FP8, int NT>
 struct KeysShape {
     static constexpr int STAGE = 2 * AttnLds<DP, FP8>::BLOCK;
     static constexpr int NW = STAGE > 16384 ? 2 : 4;
-    static constexpr int ST = STAGE > 8192 ? 2 : 4;
+    static constexpr int ST = STAGE > 8192 || (STAGE > 4096 && NT == 1) ? 2 : 4;
     static constexpr int BYTES = NW * ST * STAGE;
     static constexpr int PER_CU = BYTES <= 65536 ? 2 : 1;
 };
 
 template <int DP, bool FP8, int NT>
-__global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_kernel(AttnArgs a, int mode)
+__global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_keys_kernel(AttnArgs a, int mode)
 {
     using L = AttnLds<DP, FP8>;
-    using SH = KeysShape<DP, FP8>;
+    using SH = KeysShape<DP, FP8, NT>;
     constexpr int NW = SH::NW, ST = SH::ST, STAGE = SH::STAGE;
     constexpr int NI = 2 * L::NIH;        // load instructions of a block of K, or of V
     constexpr int QC = DP / 8;            // 8-column pieces of a row
@@ -302,16 +302,16 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8>::NW * 64)) mx_attn_keys_ke
 template <int DP, bool FP8, int NT>
 void launch(const AttnArgs &a, int plan, int grid, hipStream_t s)
 {
-    mx_attn_keys_kernel<DP, FP8, NT><<<grid, KeysShape<DP, FP8>::NW * 64, 0, s>>>(a, plan);
+    mx_attn_keys_kernel<DP, FP8, NT><<<grid, KeysShape<DP, FP8, NT>::NW * 64, 0, s>>>(a, plan);
 }
 
 template <int DP, bool FP8>
 constexpr AttnKeysKernel entry()
 {
     if constexpr (DP < 256)
-        return {{KeysShape<DP, FP8>::PER_CU, 1}, {launch<DP, FP8, 1>, launch<DP, FP8, 2>}};
+        return {{KeysShape<DP, FP8, 1>::PER_CU, KeysShape<DP, FP8, 2>::PER_CU}, {launch<DP, FP8, 1>, launch<DP, FP8, 2>}};
     else
-        return {{KeysShape<DP, FP8>::PER_CU, 1}, {launch<DP, FP8, 1>, nullptr}};
+        return {{KeysShape<DP, FP8, 1>::PER_CU, 1}, {launch<DP, FP8, 1>, nullptr}};
 }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }

@@ -68,6 +68,10 @@ int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
     return kv_heads * (T * group / tile + std::min<int64_t>(T, seqs));
 }
 
+// 32-row parts of the partial results of a call's workgroups (twice as many
+// have room: a workgroup may leave two)
+int64_t most_parts(int D) { return D > 128 ? 1024 : 2048; }
+
 bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 {
     return T >= 1 && T <= kMaxTokens && seqs >= 1 && seqs <= kMaxSeqs && kv_heads >= 1 && heads >= kv_heads &&
@@ -143,8 +147,8 @@ size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv
 {
     if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
         return 0;
-    const int parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? mx::kAttnRowsTile / 32 : 2;
-    return (size_t)(mx::kAttnCounterBytes + 2 * mx::kAttnPieces * parts * mx::attn_partial_floats(head_dim) * 4);
+    const int64_t parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? most_parts(head_dim) : 2 * mx::kAttnPieces;
+    return (size_t)(mx::kAttnCounterBytes + 2 * parts * mx::attn_partial_floats(head_dim) * 4);
 }
 
 mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_attention *p, int T, void *workspace,
@@ -210,7 +214,7 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     if (most_rows > kKeysRows) {
         const mx::AttnRowsKernel rows = mx::attn_rows_kernel(D, fp8, (int64_t)Hk * T * G < kLargeTiles * cu);
         const int64_t tiles = most_units(T, cache->seqs, G, Hk, rows.tile);
-        const int64_t wgs = std::min<int64_t>((int64_t)cu * rows.per_cu, mx::kAttnPieces);
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * rows.per_cu, std::min<int64_t>(mx::kAttnPieces, most_parts(D) / (rows.tile / 32)));
         if (tiles >= 2 * wgs)
             rows.launch(a, mx::kPlanWhole, (int)tiles, stream);
         else
