@@ -137,11 +137,11 @@ __device__ __forceinline__ AttnSeq load_seq(const CacheArgs &c, int T, int s)
 // Rows of a sequence, in tiles of `tile`; and the 128-key groups that a tile
 // can need (an upper bound where a window moves with the tokens)
 __device__ __forceinline__ int seq_tiles(const AttnSeq &q, int group, int tile) { return (q.n * group + tile - 1) / tile; }
-__device__ __forceinline__ int seq_groups(const AttnSeq &q, int group, int tile, int window)
+__device__ __forceinline__ int seq_groups(const AttnArgs &a, const AttnSeq &q, int tile)
 {
     int n = (q.len + kAttnGroup - 1) / kAttnGroup;
-    if (window > 0) {
-        const int64_t most = (int64_t)window + tile / group + 1;
+    if (a.window > 0 && a.causal) {
+        const int64_t most = (int64_t)a.window + tile / a.group + 1;
         n = (int)min((int64_t)n, (most + kAttnGroup - 1) / kAttnGroup + 1);
     }
     return max(n, 1);

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_key
         int lo, hi;
         tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
-        const int b0 = max(keys.lo, lo) / 32, b1 = (keys.hi + 31) / 32;
+        const int b0 = max(keys.lo, lo) / 32, b1 = keys.lo < keys.hi ? (keys.hi + 31) / 32 : b0;  // (a step behind the last key: none)
         const int nb = max((b1 - b0 - wave + NW - 1) / NW, 0);  // this wave's blocks: b0 + wave, + NW, ...
 
         const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;

@@ -31,7 +31,7 @@ struct AttnPlan {
 
 __device__ __forceinline__ int seq_steps(const AttnArgs &a, const AttnSeq &q, int tile, int per)
 {
-    return (seq_groups(q, a.group, tile, a.window) + per - 1) / per;
+    return (seq_groups(a, q, tile) + per - 1) / per;
 }
 __device__ __forceinline__ int seq_units(const AttnArgs &a, const AttnSeq &q, int tile)
 {

@@ -333,24 +333,57 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
             done = split_arrive_last_via(end_args.counters + first, last - first + 1, &s_last);
             if (done && wrows > 0) {
                 const int off = unit_start > first * plan.chunk ? 1 : 0;
-                t.reset();
-                for (int w = 0; w <= last - first; ++w) {
-                    const __amdgpu_buffer_rsrc_t from = make_rsrc_u(
-                        end_args.partials + (2 * (int64_t)(first + w) + (w == 0 ? off : 0)) * (NW * PW) + wave * PW, PW * 4);
-                    const v2u ml = __builtin_amdgcn_raw_buffer_load_b64(from, (uint32_t)(L::ND * 16 * 256 + end_lane * 8), 0, kCoherent);
-                    const float mw = __uint_as_float(ml[0]), n = fmaxf(t.m, mw);
-                    const float f0 = n == kNegInf ? 1.0f : exp2_fast(t.m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
-                    t.m = n;
-                    t.l = t.l * f0 + __uint_as_float(ml[1]) * f1;
+                const int parts = last - first + 1;
+                auto part = [&](int w) __attribute__((always_inline)) {
+                    return make_rsrc_u(end_args.partials + (2 * (int64_t)(first + w) + (w == 0 ? off : 0)) * (NW * PW) + wave * PW, PW * 4);
+                };
+                auto m_and_l = [&](int w) __attribute__((always_inline)) {
+                    return __builtin_amdgcn_raw_buffer_load_b64(part(w), (uint32_t)(L::ND * 16 * 256 + end_lane * 8), 0, kCoherent);
+                };
+                // first what the parts' maxima and sums come to, then O by 32
+                // columns: PB parts in flight (one after another 64 parts took 300 us)
+                constexpr int PB = 2;
+                float m = kNegInf;
+                t.l = 0.0f;
+                for (int w0 = 0; w0 < parts; w0 += PB) {
+                    v2u ml[PB];
 #pragma unroll
-                    for (int d = 0; d < L::ND; ++d)
+                    for (int i = 0; i < PB; ++i)
+                        ml[i] = m_and_l(min(w0 + i, parts - 1));
 #pragma unroll
-                        for (int g = 0; g < 16; g += 4) {
-                            const v4f x = load16_coherent(from, (uint32_t)(((d * 4 + (g >> 2)) * 64 + end_lane) * 16));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                t.o[d][g + e] = t.o[d][g + e] * f0 + x[e] * f1;
+                    for (int i = 0; i < PB; ++i)
+                        if (w0 + i < parts) {
+                            const float mw = __uint_as_float(ml[i][0]), n = fmaxf(m, mw);
+                            const float f0 = n == kNegInf ? 1.0f : exp2_fast(m - n), f1 = n == kNegInf ? 1.0f : exp2_fast(mw - n);
+                            m = n;
+                            t.l = t.l * f0 + __uint_as_float(ml[i][1]) * f1;
                         }
+                }
+                t.m = m;
+#pragma unroll
+                for (int d = 0; d < L::ND; ++d) {
+                    t.o[d] = v16f{};
+#pragma unroll 1
+                    for (int w0 = 0; w0 < parts; w0 += PB) {
+                        v2u ml[PB];
+                        v4f y[PB][4];
+#pragma unroll
+                        for (int i = 0; i < PB; ++i)
+                            if (w0 + i < parts) {
+                                ml[i] = m_and_l(w0 + i);
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    y[i][g] = load16_coherent(part(w0 + i), (uint32_t)(((d * 4 + g) * 64 + end_lane) * 16));
+                            }
+#pragma unroll
+                        for (int i = 0; i < PB; ++i)
+                            if (w0 + i < parts) {
+                                const float f = m == kNegInf ? 1.0f : exp2_fast(__uint_as_float(ml[i][0]) - m);
+#pragma unroll
+                                for (int g = 0; g < 16; ++g)
+                                    t.o[d][g] = fmaf(y[i][g >> 2][g & 3], f, t.o[d][g]);
+                            }
+                    }
                 }
             }
         }

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "mx_attention.hpp"
 #include "mx_host.hpp"
@@ -17,7 +18,6 @@ constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxSeqs = 1 << 16;
 constexpr int kMaxHeads = 512;  // of queries, keys and values together
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
-constexpr int kKeysRows = 64;   // rows of a sequence and key head up to which its waves share a tile
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -60,8 +60,6 @@ mxgemm_status check_cache(const mxgemm_kv_cache *c, bool pages, mx::CacheArgs &a
     return MXGEMM_OK;
 }
 
-constexpr int64_t kLargeTiles = 256;  // rows (all heads) per compute unit from which the large shape is taken
-
 // Tiles of `tile` rows over all sequences and key heads, at most
 int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
 {
@@ -76,6 +74,57 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 {
     return T >= 1 && T <= kMaxTokens && seqs >= 1 && seqs <= kMaxSeqs && kv_heads >= 1 && heads >= kv_heads &&
            heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && (int64_t)T * (heads / kv_heads) <= kMaxInt / 2 && D >= 32 && D <= 256 && D % 32 == 0;
+}
+
+// Which kernel, and how its work is handed out.
+//   - Few rows of a sequence and key head: the waves of a workgroup share 32 or 64
+//     rows and take keys in turn.  Up to 256 rows this also holds where the other
+//     kernel has fewer tiles than there are compute units, although keys are then
+//     read once per 64 rows: us, keys / rows kernel, 8 key heads of 4 query heads,
+//     D = 128: 32 tokens over 8192 38 / 305, 64 over 32768 74 / 188, 8 x 16 over
+//     16384 88 / 130, but 32 x 16 over 2000 (384 tiles) 69 / 62.
+//   - Else tiles of 128 rows, or of 256 where these are one for every compute unit:
+//     512 tokens in a batch of 32 decoding ones over 4096 99 / 130, a prompt of 8192
+//     617 / 576.  (D <= 64: 128 rows always, 8000 tokens of 16 heads 68 / 80.)
+// MXGEMM_ATTENTION_KERNEL (0: keys, 32 rows; 1: keys, 64 rows; 2, 3: rows, smaller
+// and larger tiles) is the tests' choice instead.
+constexpr int kKeysFewRows = 64;
+constexpr int kKeysRows = 256;
+constexpr int kLargeRows = 256;  // of all heads per compute unit
+
+struct AttnChoice {
+    mx::AttnLaunchFn launch;
+    int plan, grid;
+};
+AttnChoice choose_attention(int T, int seqs, int G, int Hk, int D, bool fp8, int max_new, int64_t groups, int cu)
+{
+    const int64_t most_rows = (int64_t)(max_new > 0 ? std::min(max_new, T) : T) * G;
+    const mx::AttnKeysKernel keys = mx::attn_keys_kernel(D, fp8);
+    bool small = (int64_t)Hk * T * G < (int64_t)kLargeRows * cu;
+    bool wide = most_rows > mx::kAttnTile;
+    bool few = most_rows <= kKeysFewRows ||
+               (most_rows <= kKeysRows && most_units(T, seqs, G, Hk, mx::attn_rows_kernel(D, fp8, small).tile) < cu);
+    if (const char *e = std::getenv("MXGEMM_ATTENTION_KERNEL")) {
+        const int k = std::atoi(e);
+        few = k < 2;
+        wide = k == 1;
+        small = k == 2;
+    }
+    if (few) {
+        wide = wide && keys.launch[1];
+        const int64_t tiles = most_units(T, seqs, G, Hk, wide ? 2 * mx::kAttnTile : mx::kAttnTile);
+        // few units: one workgroup a compute unit (fewer parts to add: one token over
+        // 32768 in 8 bits 19.5 us, with two 24)
+        const bool parts = 2 * tiles <= cu;
+        const int64_t wgs = std::min<int64_t>((int64_t)cu * (parts ? 1 : keys.per_cu[wide]), mx::kAttnPieces);
+        return {keys.launch[wide], parts ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs)};
+    }
+    const mx::AttnRowsKernel rows = mx::attn_rows_kernel(D, fp8, small);
+    const int64_t tiles = most_units(T, seqs, G, Hk, rows.tile);
+    const int64_t wgs = std::min<int64_t>({(int64_t)cu * rows.per_cu, mx::kAttnPieces, most_parts(D) / (rows.tile / 32)});
+    if (tiles >= 2 * wgs)
+        return {rows.launch, mx::kPlanWhole, (int)tiles};
+    return {rows.launch, mx::kPlanLine, (int)std::min(tiles * groups, wgs)};
 }
 
 }  // namespace
@@ -147,8 +196,7 @@ size_t mxgemm_paged_attention_workspace_bytes(int T, int seqs, int heads, int kv
 {
     if (!attention_shape(T, seqs, heads, kv_heads, head_dim))
         return 0;
-    const int64_t parts = (int64_t)T * (heads / kv_heads) > kKeysRows ? most_parts(head_dim) : 2 * mx::kAttnPieces;
-    return (size_t)(mx::kAttnCounterBytes + 2 * parts * mx::attn_partial_floats(head_dim) * 4);
+    return (size_t)(mx::kAttnCounterBytes + 2 * most_parts(head_dim) * mx::attn_partial_floats(head_dim) * 4);
 }
 
 mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_attention *p, int T, void *workspace,
@@ -207,23 +255,8 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     a.counters = (int *)workspace;
     a.partials = (float *)((uint8_t *)workspace + mx::kAttnCounterBytes);
     const bool fp8 = cache->format == MXGEMM_KV_FP8_E4M3;
-    const int most_new = p->max_new > 0 ? std::min(p->max_new, T) : T;
-    const mx::AttnKeysKernel keys = mx::attn_keys_kernel(D, fp8);
-    const int64_t most_rows = (int64_t)most_new * G;
-    const int tile = most_rows <= mx::kAttnTile || !keys.launch[1] ? mx::kAttnTile : 2 * mx::kAttnTile;
-    if (most_rows > kKeysRows) {
-        const mx::AttnRowsKernel rows = mx::attn_rows_kernel(D, fp8, (int64_t)Hk * T * G < kLargeTiles * cu);
-        const int64_t tiles = most_units(T, cache->seqs, G, Hk, rows.tile);
-        const int64_t wgs = std::min<int64_t>((int64_t)cu * rows.per_cu, std::min<int64_t>(mx::kAttnPieces, most_parts(D) / (rows.tile / 32)));
-        if (tiles >= 2 * wgs)
-            rows.launch(a, mx::kPlanWhole, (int)tiles, stream);
-        else
-            rows.launch(a, mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
-    } else {
-        const int64_t tiles = most_units(T, cache->seqs, G, Hk, tile);
-        const int64_t wgs = std::min<int64_t>((int64_t)cu * keys.per_cu[tile / mx::kAttnTile - 1], mx::kAttnPieces);
-        keys.launch[tile / mx::kAttnTile - 1](a, 2 * tiles <= wgs ? mx::kPlanParts : mx::kPlanLine, (int)std::min(tiles * groups, wgs), stream);
-    }
+    const AttnChoice k = choose_attention(T, cache->seqs, G, Hk, D, fp8, p->max_new, groups, cu);
+    k.launch(a, k.plan, k.grid, stream);
     return launched();
 }
 
