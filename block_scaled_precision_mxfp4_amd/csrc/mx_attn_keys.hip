@@ -51,7 +51,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_key
     const uint32_t ka = L::k_first(lds_addr(mine), lane), va = L::v_first(lds_addr(mine) + L::BLOCK, lane);
 
     AttnPlan plan;
-    if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+    if (!attn_plan(a, first_loads, TM, 1, mode, wg, gridDim.x, lane, plan))
         return;
     int at = wg * plan.chunk;
     const int end = min(at + plan.chunk, plan.total);

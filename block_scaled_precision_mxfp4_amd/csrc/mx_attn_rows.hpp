@@ -8,9 +8,15 @@
 namespace mx {
 
 // Waves of a workgroup, keys of a stage and stages in LDS.  SMALL: half the rows
-// and two workgroups (of D <= 64 three) on a compute unit, which fill each
-// other's barriers; the large shape reads keys and values half as often.
-// MEASURED
+// and two workgroups on a compute unit, which fill each other's barriers and ends;
+// the large shape reads keys and values half as often.  A prompt of 8192 tokens,
+// 32 heads of 128 (550 GFLOP of the causal half): 541 us, 1.0 PFLOP/s, where a
+// large bf16 product of the library's reaches 1.2 to 1.3; counters at 550 us: the
+// matrix units busy 46 % of the cycles, the vector units 48 %, LDS 22 %.  On one
+// SIMD the two overlap only in part (two waves of 32-cycle products with 8 vector
+// instructions to each take 335 us where the products alone take 245 and the
+// vector instructions 175), so that what is left is in the vector instructions of
+// a score: multiply-add, exponential (8 cycles), maximum, sum, half a conversion.
 template <int DP, bool SMALL>
 struct RowsShape {
     static constexpr int NW = DP == 256 || SMALL ? 4 : 8;
@@ -64,32 +70,40 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
     }
     const uint32_t ka = L::k_first(lds_addr(ring), lane), va = L::v_first(lds_addr(ring) + KT * L::ROWB, lane);
 
-    AttnPlan plan;
-    if (!attn_plan(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+    AttnTile plan;
+    if (!attn_tiles(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
         return;
-    int at = wg * plan.chunk;
-    const int end = min(at + plan.chunk, plan.total);
-    int s = plan.s, seq_start = plan.start;
-    AttnSeq q = plan.q;
-    int cost = seq_steps(a, q, TM, plan.per), units = seq_units(a, q, TM);
-    while (at < end) {
-        while (at >= seq_start + units * cost) {
-            seq_start += units * cost;
-            if (++s >= a.c.seqs)
-                return;
-            q = load_seq(a.c, a.T, s);
-            cost = seq_steps(a, q, TM, plan.per);
-            units = seq_units(a, q, TM);
+    int at = plan.at;
+    while (at < plan.end) {
+        int tile = seq_tiles(plan.q, a.group, TM) - 1 - plan.nth;  // the tiles with the most keys first
+        int steps = tile_steps(a, plan.q, tile, TM, plan), cost = unit_steps(plan, steps);
+        while (at >= plan.start + cost) {
+            plan.start += cost;
+            ++plan.nth;
+            while (--tile < 0) {
+                plan.nth = 0;
+                if (++plan.head == a.c.kv_heads) {
+                    if (++plan.s >= a.c.seqs)
+                        return;
+                    plan.q = load_seq(a.c, a.T, plan.s);
+                    plan.head = 0;
+                }
+                tile = seq_tiles(plan.q, a.group, TM);
+            }
+            steps = tile_steps(a, plan.q, tile, TM, plan);
+            cost = unit_steps(plan, steps);
         }
-        const int u = (at - seq_start) / cost, unit_start = seq_start + u * cost;
-        // the tiles with the most keys first
-        const int nth = quotient(u, a.by_kv_heads), head = u - nth * a.c.kv_heads;
-        const int tile = seq_tiles(q, a.group, TM) - 1 - nth;
-        const int piece_end = min(end, unit_start + cost);
+        const AttnSeq q = plan.q;
+        const int head = plan.head, unit_start = plan.start;
+        const int piece_end = min(plan.end, unit_start + cost);
+        if (at >= unit_start + steps) {  // (its keys are other workgroups')
+            at = piece_end;
+            continue;
+        }
         const int r0 = tile * TM, rows = min(q.n * a.group - r0, TM);
         int lo, hi;
-        tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
-        const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
+        keys_of_tile(a, q, tile, TM, lo, hi);
+        const KeyRange keys = step_keys(lo, hi, (at - unit_start), min(piece_end - unit_start, steps), plan.per);
         const int k0 = max(keys.lo, lo / KT * KT), k1 = keys.hi;
         const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
 
@@ -97,7 +111,7 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
         const int my_key = k0 + wave * RW / 16 * 16;  // the 16 keys that this wave's rows are among
         AttnPages table;
         if (nt > 0)
-            table.open(a.c, s, my_key >> a.c.page_shift, s_pages[wave], lane);
+            table.open(a.c, plan.s, my_key >> a.c.page_shift, s_pages[wave], lane);
         v2u kr[PPW], vr[PPW];
         // loads of stage i: into LDS, or (8 bits) into registers
         auto issue = [&](int i) __attribute__((always_inline)) {
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
         const int end_lane = anew(lane);
         t.l = row_sum(t.l);
         __syncthreads();  // the ring is free
-        const int first = unit_start / plan.chunk, last = (unit_start + cost - 1) / plan.chunk;
+        const int first = unit_start / plan.chunk, last = (unit_start + steps - 1) / plan.chunk;  // its workgroups
         bool done = first == last;
         if (!done) {
             // a partial result: a wave's registers as they are

@@ -83,14 +83,18 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 //     read once per 64 rows: us, keys / rows kernel, 8 key heads of 4 query heads,
 //     D = 128: 32 tokens over 8192 38 / 305, 64 over 32768 74 / 188, 8 x 16 over
 //     16384 88 / 130, but 32 x 16 over 2000 (384 tiles) 69 / 62.
-//   - Else tiles of 128 rows, or of 256 where these are one for every compute unit:
-//     512 tokens in a batch of 32 decoding ones over 4096 99 / 130, a prompt of 8192
-//     617 / 576.  (D <= 64: 128 rows always, 8000 tokens of 16 heads 68 / 80.)
+//   - Else tiles of 128 rows, two workgroups on a compute unit, or of 256 where
+//     sequences have many new tokens and room for long contexts: us, 128 / 256 rows,
+//     32 query and 8 key heads of 128: 512 tokens over 8192 98 / 91, 2048 over 30720
+//     in 8 bits 1155 / 999, a prompt of 8192 561 / 541, but 8 prompts of 500 47 / 53,
+//     512 tokens in a batch of 32 decoding ones over 4096 95 / 126.  (D <= 64: 128
+//     rows always, 8000 tokens of 16 heads 68 / 80; D > 128: 128 rows of 4 waves.)
 // MXGEMM_ATTENTION_KERNEL (0: keys, 32 rows; 1: keys, 64 rows; 2, 3: rows, smaller
 // and larger tiles) is the tests' choice instead.
 constexpr int kKeysFewRows = 64;
 constexpr int kKeysRows = 256;
-constexpr int kLargeRows = 256;  // of all heads per compute unit
+constexpr int kLargeRows = 1024;  // of a sequence and key head, on average
+constexpr int kLargeKeys = 2048;  // that a sequence has room for
 
 struct AttnChoice {
     mx::AttnLaunchFn launch;
@@ -100,7 +104,7 @@ AttnChoice choose_attention(int T, int seqs, int G, int Hk, int D, bool fp8, int
 {
     const int64_t most_rows = (int64_t)(max_new > 0 ? std::min(max_new, T) : T) * G;
     const mx::AttnKeysKernel keys = mx::attn_keys_kernel(D, fp8);
-    bool small = (int64_t)Hk * T * G < (int64_t)kLargeRows * cu;
+    bool small = (int64_t)T * G < (int64_t)kLargeRows * seqs || groups * mx::kAttnGroup <= kLargeKeys;
     bool wide = most_rows > mx::kAttnTile;
     bool few = most_rows <= kKeysFewRows ||
                (most_rows <= kKeysRows && most_units(T, seqs, G, Hk, mx::attn_rows_kernel(D, fp8, small).tile) < cu);
@@ -222,7 +226,7 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     const int G = H / Hk;
     const int64_t units = most_units(T, cache->seqs, G, Hk, mx::kAttnTile);
     const int64_t groups = cdiv((int64_t)cache->max_pages * cache->page_size, mx::kAttnGroup);
-    if (units > kMaxInt / groups)
+    if (units > kMaxInt / (groups + mx::kAttnUnitSteps))
         return MXGEMM_ERR_SHAPE;
     const size_t need = mxgemm_paged_attention_workspace_bytes(T, cache->seqs, H, Hk, D);
     if (!workspace || workspace_bytes < need)

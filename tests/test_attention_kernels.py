@@ -153,3 +153,31 @@ def test_a_column_block_of_a_wider_cache():
     mx.mxgemm_paged_attention(cache, b.T, dev_bf16(q), O, heads=4, scale=128 ** -0.5, lse=lse, ldq=512, ldo=512, workspace=w,
                               workspace_bytes=w.numel())
     check(b, q, 4, (host_bits(O).reshape(b.T, 4, 128), lse.cpu().numpy()))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("seqs", [64, 65, 130])
+def test_many_sequences_of_each_kernel(seqs, kernel, monkeypatch):
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(47)
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 40], seqs)]
+    lens = [max(n + int(rng.integers(-3, 200)), 0) for n in new]
+    b = Batch(rng, new, lens, 1, 64, 16, False)
+    q = bf16(rng, b.T, 4 * 64)
+    say("case sequences", seqs, kernel)
+    check(b, q, 4, attend(b, q, 4))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
+def test_more_units_than_workgroups(causal, window, kernel, monkeypatch):
+    """Units that go out whole, by their keys: every one is done once."""
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(48)
+    new = [1, 40, 7, 0, 33, 2, 1, 64, 5, 5, 90, 1, 3, 20, 8, 11, 0, 30, 2, 1, 9, 17, 4, 1, 6, 25, 1, 2, 3, 1, 50, 4]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(-4, 300, len(new)))]
+    lens = [max(x, 0) for x in lens]
+    b = Batch(rng, new, lens, 64, 32, 16, causal, "token")
+    q = bf16(rng, b.T, 64 * 32)
+    say("case units", causal, window, kernel)
+    check(b, q, 64, attend(b, q, 64, causal=causal, window=window), causal=causal, window=window)
