@@ -63,7 +63,7 @@ mxgemm_status check_cache(const mxgemm_kv_cache *c, bool pages, mx::CacheArgs &a
 // Tiles of `tile` rows over all sequences and key heads, at most
 int64_t most_units(int64_t T, int seqs, int group, int kv_heads, int tile)
 {
-    return kv_heads * (T * group / tile + std::min<int64_t>(T, seqs));
+    return kv_heads * ((T * group + std::min<int64_t>(T, seqs) * (tile - 1)) / tile);
 }
 
 // 32-row parts of the partial results of a call's workgroups (twice as many
@@ -83,6 +83,10 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 //     read once per 64 rows: us, keys / rows kernel, 8 key heads of 4 query heads,
 //     D = 128: 32 tokens over 8192 38 / 305, 64 over 32768 74 / 188, 8 x 16 over
 //     16384 88 / 130, but 32 x 16 over 2000 (384 tiles) 69 / 62.
+//     64 rows read the keys half as often, but a tile of them that is cut into many
+//     parts takes long to add up by one workgroup: us, 32 / 64 rows, 40 rows of 64
+//     heads over 16384 in 8 bits 42 / 36, 192 rows of 8 heads over 32768 75 / 65, but
+//     128 rows over 8192 23 / 37 and 64 over 32768 43 / 58 (16 and 32 parts).
 //   - Else tiles of 128 rows, two workgroups on a compute unit, or of 256 where
 //     sequences have many new tokens and room for long contexts: us, 128 / 256 rows,
 //     32 query and 8 key heads of 128: 512 tokens over 8192 98 / 91, 2048 over 30720
@@ -93,6 +97,7 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 // and larger tiles) is the tests' choice instead.
 constexpr int kKeysFewRows = 64;
 constexpr int kKeysRows = 256;
+constexpr int kWideParts = 12;    // that a tile of 64 rows is cut into, at most
 constexpr int kLargeRows = 1024;  // of a sequence and key head, on average
 constexpr int kLargeKeys = 2048;  // that a sequence has room for
 
@@ -105,7 +110,7 @@ AttnChoice choose_attention(int T, int seqs, int G, int Hk, int D, bool fp8, int
     const int64_t most_rows = (int64_t)(max_new > 0 ? std::min(max_new, T) : T) * G;
     const mx::AttnKeysKernel keys = mx::attn_keys_kernel(D, fp8);
     bool small = (int64_t)T * G < (int64_t)kLargeRows * seqs || groups * mx::kAttnGroup <= kLargeKeys;
-    bool wide = most_rows > mx::kAttnTile;
+    bool wide = most_rows > mx::kAttnTile && (int64_t)T * G * Hk * kWideParts >= (int64_t)2 * mx::kAttnTile * cu;
     bool few = most_rows <= kKeysFewRows ||
                (most_rows <= kKeysRows && most_units(T, seqs, G, Hk, mx::attn_rows_kernel(D, fp8, small).tile) < cu);
     if (const char *e = std::getenv("MXGEMM_ATTENTION_KERNEL")) {
