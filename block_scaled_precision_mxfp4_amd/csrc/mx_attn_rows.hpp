@@ -45,7 +45,6 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wg = blockIdx.x;
     const AttnFirst first_loads = attn_first(a, lane);
 
     // this lane's places in the cache's rows and in a stage
@@ -71,8 +70,9 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
     const uint32_t ka = L::k_first(lds_addr(ring), lane), va = L::v_first(lds_addr(ring) + KT * L::ROWB, lane);
 
     AttnTile plan;
-    if (!attn_tiles(a, first_loads, TM, mode, wg, gridDim.x, lane, plan))
+    if (!attn_tiles(a, first_loads, TM, mode, blockIdx.x, gridDim.x, lane, plan))
         return;
+    const int wg = plan.wg;
     int at = plan.at;
     while (at < plan.end) {
         int tile = seq_tiles(plan.q, a.group, TM) - 1 - plan.nth;  // the tiles with the most keys first
