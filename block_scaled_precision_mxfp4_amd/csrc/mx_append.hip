@@ -1,6 +1,9 @@
 // Rotary positions and the append to a paged cache (gfx950): queries and keys
 // of new tokens are turned to their positions, queries written out, keys and
-// values written into their pages, each read once.  Bound by HBM.
+// values written into their pages, each read once.  Bound by HBM: 16384 tokens of
+// 32 + 2 x 8 heads of 128, 403 MB read and written: 92 us, 4.4 TB/s (a large copy:
+// 4.7).  One token takes 3.4 us, 509 tokens 6.2: latency of the search of the
+// offsets, the positions, the angles and the rows, one after another.
 //
 // A workgroup has a few tokens.  One wave per token finds its sequence (a
 // 64-way search of the offsets), its position and its page; the angles, which

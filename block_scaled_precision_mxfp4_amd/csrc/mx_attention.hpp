@@ -53,7 +53,7 @@ void launch_append(const AppendArgs &a, int num_cu, hipStream_t s);
 // ---- attention
 constexpr int kAttnTile = 32;    // rows (token, head of a group) that a wave holds
 constexpr int kAttnGroup = 128;  // keys that work is handed out by
-constexpr int kAttnUnitSteps = 2;  // steps that a unit of the rows kernel counts beside its keys
+constexpr int kAttnUnitSteps = 2;  // that a unit of the rows kernel counts beside its keys' (mx_attn_plan.hpp)
 constexpr int kAttnPieces = 512; // workgroups that may leave partial results, at most
 constexpr int kAttnCounterBytes = 4096;
 constexpr int kPlanWhole = 0, kPlanLine = 1, kPlanParts = 2;  // mx_attn_plan.hpp

@@ -17,8 +17,9 @@
 // read from LDS in P's order (transposed reads, whose rows each lane names).
 //
 // The scores are scaled by c = scale * k_scale * log2(e), p = 2^(c s - m).
-// P is rounded to bf16 for the second product (2^-9 of each p, which leaves
-// the result about as far off as its own rounding to bf16 does); the sum adds
+// P is rounded to bf16 for the second product (up to 2^-8 of each p, which leaves
+// the result about as far off as its own rounding to bf16 does: measured 0.0022 of
+// the exact result's norm with both, 0.0017 with the last alone); the sum adds
 // the unrounded p in fp32.  The running maximum is raised only where it grows
 // by more than 8 (p up to 2^8): all of O would have to be rescaled otherwise.
 #pragma once
