@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxSeqs = 1 << 16;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;  // T * heads of an attention (its grids have up to 2^31 threads)
 constexpr int kMaxHeads = 512;  // of queries, keys and values together
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
@@ -73,7 +74,7 @@ int64_t most_parts(int D) { return D > 128 ? 1024 : 2048; }
 bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 {
     return T >= 1 && T <= kMaxTokens && seqs >= 1 && seqs <= kMaxSeqs && kv_heads >= 1 && heads >= kv_heads &&
-           heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && (int64_t)T * (heads / kv_heads) <= kMaxInt / 2 && D >= 32 && D <= 256 && D % 32 == 0;
+           heads + 2 * kv_heads <= kMaxHeads && heads % kv_heads == 0 && (int64_t)T * heads <= kMaxRows && D >= 32 && D <= 256 && D % 32 == 0;
 }
 
 // Which kernel, and how its work is handed out.
@@ -170,7 +171,7 @@ mxgemm_status mxgemm_kv_append(const mxgemm_kv_cache *cache, const mxgemm_append
         return st;
     const int D = cache->head_dim, Hk = cache->kv_heads, H = p->Q ? p->heads : 0;
     if (T < 1 || T > kMaxTokens || (p->Q && H < 1) || H > kMaxHeads || H + 2 * Hk > kMaxHeads || p->rot_dim < 0 || p->rot_dim > D || p->rot_dim % 16 ||
-        (p->Q && (p->ldq < (int64_t)H * D || p->ldqo < (int64_t)H * D)) ||
+        (p->Q && (p->ldq < (int64_t)H * D || p->ldqo < (int64_t)H * D || (p->Q == p->Q_out && p->ldq != p->ldqo))) ||
         (p->K && (p->ldk < (int64_t)Hk * D || p->ldv < (int64_t)Hk * D)))
         return MXGEMM_ERR_SHAPE;
     if (!aligned(p->Q, 16) || !aligned(p->Q_out, 16) || !aligned(p->K, 16) || !aligned(p->V, 16) ||
@@ -223,7 +224,7 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
         return st;
     const int D = cache->head_dim, Hk = cache->kv_heads, H = p->heads;
     if (!attention_shape(T, cache->seqs, H, Hk, D) || p->window < 0 || p->max_new < 0 || p->ldq < (int64_t)H * D ||
-        (p->O && p->ldo < (int64_t)H * D) || (p->A && (p->lda < (int64_t)H * D || p->ldsa < H * D / 32)))
+        (p->O && (p->ldo < (int64_t)H * D || (p->O == p->Q && p->ldo != p->ldq))) || (p->A && (p->lda < (int64_t)H * D || p->ldsa < H * D / 32)))
         return MXGEMM_ERR_SHAPE;
     if (!aligned(p->Q, 16) || p->ldq % 8 || !aligned(p->O, 16) || (p->O && p->ldo % 8) || !aligned(p->lse, 4) ||
         !aligned(p->sinks, 4) || !aligned(p->A, 16) || (p->A && p->lda % (128 / bits)))

@@ -148,6 +148,17 @@ def test_work_that_would_not_be_countable_is_refused():
     assert attention(big, T=1) in REACHED
 
 
+def test_outputs_in_place_with_other_strides_are_refused():
+    assert append(Q_out=0x10000, ldqo=264) == SHAPE
+    assert attention(O=0x10000, ldo=264) == SHAPE
+    assert append(Q_out=0x10000) in REACHED and attention(O=0x10000) in REACHED
+
+
+def test_more_rows_than_a_grid_has_are_refused():
+    assert mx.mxgemm_paged_attention_workspace_bytes(1 << 24, 1, 64, 64, 32) > 0
+    assert mx.mxgemm_paged_attention_workspace_bytes(1 << 24, 1, 65, 65, 32) == 0
+
+
 @pytest.mark.parametrize("shape", [(0, 1, 4, 2, 64), (1, 0, 4, 2, 64), (1, 1, 4, 3, 64), (1, 1, 4, 2, 65), (1, 1, 2, 4, 64), (1 << 25, 1, 4, 2, 64)])
 def test_workspace_of_an_invalid_shape(shape):
     assert mx.mxgemm_paged_attention_workspace_bytes(*shape) == 0

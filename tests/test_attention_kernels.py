@@ -181,3 +181,55 @@ def test_more_units_than_workgroups(causal, window, kernel, monkeypatch):
     q = bf16(rng, b.T, 64 * 32)
     say("case units", causal, window, kernel)
     check(b, q, 64, attend(b, q, 64, causal=causal, window=window), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("page", [512, 4096, 65536])
+def test_large_pages_and_a_wider_table(page, kernel, monkeypatch):
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(49)
+    b = Batch(rng, [1, 3], [70000, 5000], 1, 64, page, False, spare=1)
+    q = bf16(rng, b.T, 2 * 64)
+    b.cache()
+    table = np.full((2, b.max_pages + 5), 2 ** 30, np.int32)
+    table[:, :b.max_pages] = b.pages
+    table = dev(table)
+    cache = mx.make_kv_cache(b.k, b.v, table, b.dev[1], b.dev[2], seqs=2, num_pages=b.num_pages, page_size=page,
+                             max_pages=b.max_pages, ld_pages=b.max_pages + 5, kv_heads=1, head_dim=64)
+    w = workspace(b.T, 2, 2, 1, 64)
+    O = dev_bf16(np.zeros((b.T, 128), np.uint16))
+    lse = torch.zeros((b.T, 2), device="cuda")
+    say("case pages", page, kernel)
+    mx.mxgemm_paged_attention(cache, b.T, dev_bf16(q), O, heads=2, scale=0.125, lse=lse, ldq=128, ldo=128, workspace=w,
+                              workspace_bytes=w.numel())
+    check(b, q, 2, (host_bits(O).reshape(b.T, 2, 64), lse.cpu().numpy()))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rows_that_see_a_nan(kernel, monkeypatch):
+    """A NaN among a row's keys or its query makes that row NaN, also where nothing else is seen; no other row."""
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(50)
+    b = Batch(rng, [1, 50, 2], [1, 60, 900], 1, 64, 16, False)
+    q = bf16(rng, b.T, 2 * 64)
+    b.kc[b.pages[0, 0], 0, 0, 3] = 0x7FC0   # the only key of the first row
+    b.kc[b.pages[1, 2], 0, 8, 1] = 0x7FC0   # key 40: rows of positions 40 to 59
+    b.vc[b.pages[1, 3], 0, 2, 5] = 0x7F80   # value 50, column 5
+    q[51, 2] = 0x7FC0                       # the first head of a row of 900 keys
+    say("case nan", kernel)
+    check(b, q, 2, attend(b, q, 2))
+    sinks = np.array([0.0, -np.inf])
+    check(b, q, 2, attend(b, q, 2, sinks=sinks), sinks=sinks)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_more_units_than_workgroups_of_many_sequences(kernel, monkeypatch):
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(51)
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 20], 140)]
+    lens = [max(n + int(rng.integers(-2, 60)), 0) for n in new]
+    b = Batch(rng, new, lens, 8, 32, 16, False)
+    q = bf16(rng, b.T, 8 * 32)
+    say("case many units", kernel)
+    check(b, q, 8, attend(b, q, 8))
+    check(b, q, 8, attend(b, q, 8, window=9), window=9)
