@@ -233,3 +233,22 @@ def test_more_units_than_workgroups_of_many_sequences(kernel, monkeypatch):
     say("case many units", kernel)
     check(b, q, 8, attend(b, q, 8))
     check(b, q, 8, attend(b, q, 8, window=9), window=9)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_bad_tables_of_each_kernel(kernel, monkeypatch):
+    """Values mean nothing then; no address outside is formed and a later call is right."""
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(52)
+    b = Batch(rng, [1, 150, 7, 1], [50, 160, 70, 80], 1, 64, 16, False)
+    q = bf16(rng, b.T, 2 * 64)
+    w = workspace(b.T, 4, 2, 1, 64)
+    good = b.offsets.copy(), b.lens.copy(), b.pages.copy()
+    for bad in ([0, 159, 0, 159, 0], [3, 1, 9, -5, 2], [2 ** 31 - 1, -2 ** 31, 0, 159, 159], [0, 1, 2, 3, 1000]):
+        b.offsets = np.array(bad, np.int32)
+        b.lens = np.array([2 ** 31 - 1, -7, 70, 10 ** 6], np.int32)
+        b.pages = np.where(rng.random(b.pages.shape) < 0.5, 2 ** 31 - 1, b.pages).astype(np.int32)
+        say("case tables", kernel, bad)
+        attend(b, q, 2, w=w)
+    b.offsets, b.lens, b.pages = good
+    check(b, q, 2, attend(b, q, 2, w=w))
