@@ -79,11 +79,14 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 
 // Which kernel, and how its work is handed out.
 //   - Few rows of a sequence and key head: the waves of a workgroup share 32 or 64
-//     rows and take keys in turn.  Up to 256 rows this also holds where the other
-//     kernel has fewer tiles than there are compute units, although keys are then
+//     rows and take keys in turn.  Up to 512 rows (256 where 64 do not fit the
+//     registers) this also holds where all rows would fill tiles of the other
+//     kernel for less than a fifth of the compute units, although keys are then
 //     read once per 64 rows: us, keys / rows kernel, 8 key heads of 4 query heads,
-//     D = 128: 32 tokens over 8192 38 / 305, 64 over 32768 74 / 188, 8 x 16 over
-//     16384 88 / 130, but 32 x 16 over 2000 (384 tiles) 69 / 62.
+//     D = 128: 64 tokens over 32768 68 / 104, 100 over 8192 41 / 55, 8 x 16 over
+//     16384 87 / 96, 128 over 32768 110 / 119, 4 x 48 over 8192 (48 tiles) 64 / 64,
+//     but 3 x 100 over 8192 (75) 97 / 64, 8 x 48 (96) 127 / 83, 16 x 20 over 4096
+//     (80) 73 / 59.
 //     64 rows read the keys half as often, but a tile of them that is cut into many
 //     parts takes long to add up by one workgroup: us, 32 / 64 rows, 40 rows of 64
 //     heads over 16384 in 8 bits 42 / 36, 192 rows of 8 heads over 32768 75 / 65, but
@@ -97,7 +100,7 @@ bool attention_shape(int T, int seqs, int heads, int kv_heads, int D)
 // MXGEMM_ATTENTION_KERNEL (0: keys, 32 rows; 1: keys, 64 rows; 2, 3: rows, smaller
 // and larger tiles) is the tests' choice instead.
 constexpr int kKeysFewRows = 64;
-constexpr int kKeysRows = 256;
+constexpr int kKeysRows = 512;
 constexpr int kWideParts = 12;    // that a tile of 64 rows is cut into, at most
 constexpr int kLargeRows = 1024;  // of a sequence and key head, on average
 constexpr int kLargeKeys = 2048;  // that a sequence has room for
@@ -113,7 +116,8 @@ AttnChoice choose_attention(int T, int seqs, int G, int Hk, int D, bool fp8, int
     bool small = (int64_t)T * G < (int64_t)kLargeRows * seqs || groups * mx::kAttnGroup <= kLargeKeys;
     bool wide = most_rows > mx::kAttnTile && (int64_t)T * G * Hk * kWideParts >= (int64_t)2 * mx::kAttnTile * cu;
     bool few = most_rows <= kKeysFewRows ||
-               (most_rows <= kKeysRows && most_units(T, seqs, G, Hk, mx::attn_rows_kernel(D, fp8, small).tile) < cu);
+               (most_rows <= (keys.launch[1] ? kKeysRows : kKeysRows / 2) &&
+                5 * (int64_t)T * G * Hk <= (int64_t)cu * mx::attn_rows_kernel(D, fp8, small).tile);
     if (const char *e = std::getenv("MXGEMM_ATTENTION_KERNEL")) {
         const int k = std::atoi(e);
         few = k < 2;
