@@ -117,7 +117,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_key
             my[n] = attn_row(a, r0 + min(n * 32 + row, rows - 1), head);
             const int pos = q.len - q.n + my[n].token;
             row_hi[n] = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
-            row_lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+            row_lo[n] = first_key(a, pos);
         }
         if (nb > 0) {
             table.open(a.c, s, ((b0 + wave) * 32) >> a.c.page_shift, s_pages[wave], lane);

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
         const AttnRow my = attn_row(a, rr, head);
         const int idx = my.token, pos = q.len - q.n + idx;
         const int row_hi = a.causal ? min(pos + 1, q.len) : (pos < 0 ? 0 : q.len);
-        const int row_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        const int row_lo = first_key(a, pos);
         // keys that every row of the wave sees, and that some see
         const int all_lo = a.window > 0 ? __builtin_amdgcn_readlane(row_lo, 31) : 0;
         const int all_hi = __builtin_amdgcn_readlane(row_hi, 0);
