@@ -135,12 +135,15 @@ __device__ __forceinline__ AttnSeq load_seq(const CacheArgs &c, int T, int s)
     return seq_from(c, T, load_uniform(c.offsets + s), load_uniform(c.offsets + s + 1), load_uniform(c.lens + s));
 }
 
+// Blocks of `size` that hold n keys: a length may be as close to 2^31 as 16
+__device__ __forceinline__ int key_blocks(int n, int size) { return (int)(((uint32_t)n + (uint32_t)(size - 1)) / (uint32_t)size); }
+
 // Rows of a sequence, in tiles of `tile`; and the 128-key groups that a tile
 // can need (an upper bound where a window moves with the tokens)
 __device__ __forceinline__ int seq_tiles(const AttnSeq &q, int group, int tile) { return (q.n * group + tile - 1) / tile; }
 __device__ __forceinline__ int seq_groups(const AttnArgs &a, const AttnSeq &q, int tile)
 {
-    int n = (q.len + kAttnGroup - 1) / kAttnGroup;
+    int n = key_blocks(q.len, kAttnGroup);
     if (a.window > 0 && a.causal) {
         const int64_t most = (int64_t)a.window + tile / a.group + 1;
         n = (int)min((int64_t)n, (most + kAttnGroup - 1) / kAttnGroup + 1);
@@ -244,14 +247,15 @@ struct AttnLds {
 
 // 16 keys from key0 on: descriptors of K's and V's rows that exist (the others
 // read as zeros).  k, v: the key head's rows in page 0.  page: as the table has it.
+// Loads ahead of the last key may be past 2^31: they name key0 as the length too.
 struct AttnRows {
     __amdgpu_buffer_rsrc_t k, v;
 };
-__device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, const uint8_t *k, const uint8_t *v, int page, int key0, int len)
+__device__ __forceinline__ AttnRows attn_rows(const CacheArgs &c, const uint8_t *k, const uint8_t *v, int page, uint32_t key0, uint32_t len)
 {
     const bool there = (uint32_t)page < (uint32_t)c.num_pages;
-    const int rows = there ? min(max(len - key0, 0), 16) : 0;
-    const int64_t at = (int64_t)(there ? page : 0) * c.page_b + (uint32_t)(key0 & ((1 << c.page_shift) - 1)) * (uint32_t)c.token_b;
+    const int rows = there ? min(max((int)(len - key0), 0), 16) : 0;
+    const int64_t at = (int64_t)(there ? page : 0) * c.page_b + (key0 & ((1u << c.page_shift) - 1)) * (uint32_t)c.token_b;
     const uint32_t bytes = (uint32_t)rows * (uint32_t)c.token_b;
     return {make_rsrc_u(k + at, bytes), make_rsrc_u(v + at, bytes)};
 }

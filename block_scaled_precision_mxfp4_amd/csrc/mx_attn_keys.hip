@@ -80,15 +80,15 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_key
         int lo, hi;
         tile_keys(a, q, quotient(r0, a.by_group), quotient(r0 + rows - 1, a.by_group), lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), (piece_end - unit_start), plan.per);
-        const int b0 = max(keys.lo, lo) / 32, b1 = keys.lo < keys.hi ? (keys.hi + 31) / 32 : b0;  // (a step behind the last key: none)
+        const int b0 = max(keys.lo, lo) / 32, b1 = keys.lo < keys.hi ? key_blocks(keys.hi, 32) : b0;  // (a step behind the last key: none)
         const int nb = max((b1 - b0 - wave + NW - 1) / NW, 0);  // this wave's blocks: b0 + wave, + NW, ...
 
         const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
         AttnPages table;
         auto issue = [&](int i) __attribute__((always_inline)) {
-            const int key0 = (b0 + wave + i * NW) * 32, len = i < nb ? q.len : 0;
+            const uint32_t key0 = (uint32_t)(b0 + wave + i * NW) * 32, len = i < nb ? q.len : key0;
             int pg0, pg1;
-            table.get(key0 >> a.c.page_shift, (key0 + 16) >> a.c.page_shift, lane, pg0, pg1);
+            table.get((int)(key0 >> a.c.page_shift), (int)((key0 + 16) >> a.c.page_shift), lane, pg0, pg1);
             const AttnRows x = attn_rows(a.c, k_head, v_head, pg0, key0, len);
             const AttnRows y = attn_rows(a.c, k_head, v_head, pg1, key0 + 16, len);
             uint8_t *to = mine + (i % ST) * STAGE;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__((KeysShape<DP, FP8, NT>::NW * 64)) mx_attn_key
                 attn_wait_vm<NI + (ST - 1) * 2 * NI>();
                 v16f x[NT];
                 scores<DP, FP8, NT>(ka + slot, qf, x);
-                const bool masked = key0 < all_lo || key0 + 32 > all_hi;
+                const bool masked = key0 < all_lo || all_hi - key0 < 32;
                 int lo_b[NT], hi_b[NT];
                 v4i p[NT][2];
 #pragma unroll

@@ -197,7 +197,7 @@ __device__ __forceinline__ int tile_steps(const AttnArgs &a, const AttnSeq &q, i
         return seq_steps(a, q, size, p.per);
     int lo, hi;
     keys_of_tile(a, q, tile, size, lo, hi);
-    return max((hi + kAttnGroup - 1) / kAttnGroup - lo / kAttnGroup, 1);
+    return max(key_blocks(hi, kAttnGroup) - lo / kAttnGroup, 1);
 }
 
 // Steps of one unit: those with keys and the others

@@ -105,20 +105,21 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
         keys_of_tile(a, q, tile, TM, lo, hi);
         const KeyRange keys = step_keys(lo, hi, (at - unit_start), min(piece_end - unit_start, steps), plan.per);
         const int k0 = max(keys.lo, lo / KT * KT), k1 = keys.hi;
-        const int nt = max((k1 - k0 + KT - 1) / KT, 0);  // stages
+        const int nt = k1 > k0 ? key_blocks(k1 - k0, KT) : 0;  // stages
 
         const uint8_t *k_head = a.c.k + head * a.c.head_b, *v_head = a.c.v + head * a.c.head_b;
-        const int my_key = k0 + wave * RW / 16 * 16;  // the 16 keys that this wave's rows are among
+        const uint32_t my_key = (uint32_t)k0 + wave * RW / 16 * 16;  // the 16 keys that this wave's rows are among
         AttnPages table;
         if (nt > 0)
-            table.open(a.c, plan.s, my_key >> a.c.page_shift, s_pages[wave], lane);
+            table.open(a.c, plan.s, (int)(my_key >> a.c.page_shift), s_pages[wave], lane);
         v2u kr[PPW], vr[PPW];
         // loads of stage i: into LDS, or (8 bits) into registers
         auto issue = [&](int i) __attribute__((always_inline)) {
-            const int key = my_key + i * KT;
+            const uint32_t key = my_key + i * KT;
+            const int entry = (int)(key >> a.c.page_shift);
             int page, same;
-            table.get(key >> a.c.page_shift, key >> a.c.page_shift, lane, page, same);
-            const AttnRows x = attn_rows(a.c, k_head, v_head, page, key, i < nt ? q.len : 0);
+            table.get(entry, entry, lane, page, same);
+            const AttnRows x = attn_rows(a.c, k_head, v_head, page, key, i < nt ? q.len : key);
             if constexpr (FP8) {
 #pragma unroll
                 for (int j = 0; j < PPW; ++j) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__((RowsShape<DP, SMALL>::NW * 64), (SMALL && DP 
         // Blocks of 32 keys, counted from k0: [s0, s1) are seen by some row of the
         // wave, [f0, f1) by all of them
         const int blocks = nt * NB;
-        const int s0 = max(any_lo - k0, 0) / 32, s1 = min((any_hi - k0 + 31) >> 5, blocks);
+        const int s0 = max(any_lo - k0, 0) / 32, s1 = min(((any_hi - k0 - 1) >> 5) + 1, blocks);
         const int f0 = (max(all_lo - k0, 0) + 31) / 32, f1 = min((all_hi - k0) >> 5, s1);
         v16f x;  // scores of the block whose exponentials are next
         auto slot = [&](int c) { return (uint32_t)((c / NB % ST) * STAGE + c % NB * L::BLOCK); };
