@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxSeqs = 1 << 16;
-constexpr int64_t kMaxRows = (int64_t)1 << 30;  // T * heads of an attention (its grids have up to 2^31 threads)
+constexpr int64_t kMaxRows = (int64_t)1 << 30;  // T * heads of an attention
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // of a launch
 constexpr int kMaxHeads = 512;  // of queries, keys and values together
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
@@ -136,7 +137,9 @@ AttnChoice choose_attention(int T, int seqs, int G, int Hk, int D, bool fp8, int
     const mx::AttnRowsKernel rows = mx::attn_rows_kernel(D, fp8, small);
     const int64_t tiles = most_units(T, seqs, G, Hk, rows.tile);
     const int64_t wgs = std::min<int64_t>({(int64_t)cu * rows.per_cu, mx::kAttnPieces, most_parts(D) / (rows.tile / 32)});
-    if (tiles >= 2 * wgs)
+    // (every sequence and key head may have a tile that is partly filled: more
+    // workgroups, of 64 threads a tile's 32 rows, than a launch can have go in line)
+    if (tiles >= 2 * wgs && tiles * 2 * rows.tile <= kMaxThreads)
         return {rows.launch, mx::kPlanWhole, (int)tiles};
     return {rows.launch, mx::kPlanLine, (int)std::min(tiles * groups, wgs)};
 }

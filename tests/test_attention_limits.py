@@ -93,3 +93,37 @@ def test_lengths_up_to_the_largest_capacity(kernel, monkeypatch):
                     full = m + np.log(total)
                     assert abs(l[t, h] - full) <= 2 * dx + 2 ** -21 + sums + 8 * ref.F32 * abs(full)
     assert not w[:4096].any()
+
+
+def test_more_tiles_than_a_launch_has_workgroups_for():
+    """65536 sequences of 170 key heads that may each end in a tile of their own: 2^24 workgroups of 256 threads would
+    be 2^32.  Few sequences have tokens; the rows behind them are left as they were (and most of them never touched)."""
+    rng = np.random.default_rng(62)
+    H, D, S, T = 170, 32, 65536, 4310000
+    assert H * ((T + S * 127) // 128) * 256 >= 2 ** 32
+    b = Batch(rng, [1, 70, 0, 3, 1], [30, 75, 5, 2, 1], H, D, 16, False)
+    q = bf16(rng, b.T, H * D, sigma=2.0)
+    b.cache()
+    at = np.array([0, 64, 65, 40000, S - 1])  # where those sequences are
+    new, lens = np.zeros(S, np.int64), np.zeros(S, np.int32)
+    new[at], lens[at] = b.new, b.lens
+    offsets = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+    pages = np.zeros((S, b.max_pages), np.int32)
+    pages[at] = b.pages
+    cache_dev = dev(pages), dev(offsets), dev(lens)
+    cache = mx.make_kv_cache(b.k, b.v, *cache_dev, seqs=S, num_pages=b.num_pages, page_size=16, max_pages=b.max_pages,
+                             kv_heads=H, head_dim=D)
+    rows = torch.empty((T, H * D), dtype=torch.bfloat16, device="cuda")  # 47 GB, in place
+    rows[:b.T] = dev_bf16(q)
+    rows[b.T:b.T + 50] = 3.0
+    w = workspace(T, S, H, H, D)
+    lse = torch.full((T, H), 77.0, device="cuda")
+    say("case tiles")
+    mx.mxgemm_paged_attention(cache, T, rows, rows, heads=H, scale=D ** -0.5, lse=lse, ldq=H * D, ldo=H * D, workspace=w,
+                              workspace_bytes=w.numel())
+    torch.cuda.synchronize()
+    assert not w[:4096].any()
+    assert (rows[b.T:b.T + 50] == 3.0).all() and (lse[b.T:] == 77).all()
+    check(b, q, H, (host_bits(rows[:b.T]).reshape(b.T, H, D), lse[:b.T].cpu().numpy()))
+    del rows, lse
+    torch.cuda.empty_cache()
