@@ -239,7 +239,8 @@ mxgemm_status mxgemm_paged_attention(const mxgemm_kv_cache *cache, const mxgemm_
     const int G = H / Hk;
     const int64_t units = most_units(T, cache->seqs, G, Hk, mx::kAttnTile);
     const int64_t groups = cdiv((int64_t)cache->max_pages * cache->page_size, mx::kAttnGroup);
-    if (units > kMaxInt / (groups + mx::kAttnUnitSteps))
+    // (the plan rounds the steps of all units up to whole workgroups in 32 bits)
+    if (units > (kMaxInt - mx::kAttnPieces) / (groups + mx::kAttnUnitSteps))
         return MXGEMM_ERR_SHAPE;
     const size_t need = mxgemm_paged_attention_workspace_bytes(T, cache->seqs, H, Hk, D);
     if (!workspace || workspace_bytes < need)

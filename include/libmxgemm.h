@@ -731,8 +731,11 @@ typedef struct mxgemm_attention {
  * can overlap.  Its first 4 KiB are counters, which every call leaves zero
  * again; the rest needs no clearing, so that calls of any sizes can use one
  * workspace in turn.  Deterministic: the same call gives the same bits.
- * 1 <= T <= 2^24, T * heads <= 2^30; bf16 pointers 16-byte aligned, their strides
- * multiples of 8; A as in mxgemm_quantize.  But for O no output overlaps an input or another output.  Errors:
+ * 1 <= T <= 2^24, T * heads <= 2^30, and U * (ceil(max_pages * page_size / 128) + 2)
+ * < 2^31 - 512, where U = kv_heads * floor((T * heads / kv_heads + 31 * min(T,
+ * seqs)) / 32) (else MXGEMM_ERR_SHAPE); bf16 pointers 16-byte aligned, their
+ * strides multiples of 8; A as in mxgemm_quantize.  But for O no output overlaps an
+ * input or another output.  Errors:
  * MXGEMM_ERR_INVALID_ARG, MXGEMM_ERR_SHAPE, MXGEMM_ERR_ALIGN,
  * MXGEMM_ERR_WORKSPACE, all before any HIP call.  Asynchronous on `stream`.
  */
