@@ -127,3 +127,27 @@ def test_more_tiles_than_a_launch_has_workgroups_for():
     check(b, q, H, (host_bits(rows[:b.T]).reshape(b.T, H, D), lse[:b.T].cpu().numpy()))
     del rows, lse
     torch.cuda.empty_cache()
+
+
+def nan_batch(rng):
+    """As in test_attention_kernels.test_rows_that_see_a_nan: NaN keys, a NaN query, an infinite value."""
+    b = Batch(rng, [1, 50, 2], [1, 60, 900], 1, 64, 16, False)
+    q = bf16(rng, b.T, 2 * 64)
+    b.kc[b.pages[0, 0], 0, 0, 3] = 0x7FC0
+    b.kc[b.pages[1, 2], 0, 8, 1] = 0x7FC0
+    b.vc[b.pages[1, 3], 0, 2, 5] = 0x7F80
+    q[51, 2] = 0x7FC0
+    return b, q
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_logarithms_of_rows_that_see_a_nan(kernel, monkeypatch):
+    """lse is NaN where a score is, and nowhere else."""
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    b, q = nan_batch(np.random.default_rng(63))
+    for sinks in (None, np.array([0.0, -np.inf])):
+        _, want, _, _ = ref.attention(ref.bf16_to_f64(q).reshape(-1, 2, 64), b.host(), 0.125, True, 0, sinks)
+        say("case nan logarithms", kernel)
+        _, lse = attend(b, q, 2, sinks=sinks)
+        assert np.isnan(want).any() and not np.isnan(want).all()
+        assert np.array_equal(np.isnan(lse), np.isnan(want))
