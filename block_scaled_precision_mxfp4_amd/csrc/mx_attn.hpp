@@ -600,7 +600,7 @@ __device__ __forceinline__ RowEnd end_row(const AttnArgs &a, int kv_head, int he
     float w = 1.0f;
     if (a.sinks) {
         const float k = a.sinks[head] * kLog2e, n = fmaxf(m, k);
-        if (n != kNegInf) {
+        if (n != kNegInf || k != k) {  // (a NaN sink: NaN, also where no key is seen)
             w = exp2_fast(m - n);
             l = l * w + exp2_fast(k - n);
             m = n;

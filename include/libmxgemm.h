@@ -703,11 +703,12 @@ mxgemm_status mxgemm_rope_frequencies(double *freq, int rot_dim, double base, do
  *     lse[t][h] = log(sum_j e^(x_j) + e^sinks[h])
  *
  * (without sinks the last terms are absent; a row without a key is 0, its lse
- * -inf or the sink).  Keys that a row does not see do not reach it, whatever
- * they or their values hold.  O is rounded once to bf16; A with scaleA are
- * those bf16 values quantized (mxgemm_quantize's rule, or MXFP8 as in "mixture
- * of experts"), blocks of 32 columns of a row.  Products are of bf16 (E4M3 codes
- * as they are), sums in fp32; e^x is rounded to bf16 for the product with v.
+ * -inf or the sink; a sink of +inf or NaN makes the rows of its head NaN).  Keys
+ * that a row does not see do not reach it, whatever they or their values hold.
+ * O is rounded once to bf16; A with scaleA are those bf16 values quantized
+ * (mxgemm_quantize's rule, or MXFP8 as in "mixture of experts"), blocks of 32
+ * columns of a row.  Products are of bf16 (E4M3 codes as they are), sums in
+ * fp32; e^x is rounded to bf16 for the product with v.
  */
 typedef struct mxgemm_attention {
     const void *Q;      /* bf16 [T][ldq], head h from column h * head_dim */

@@ -151,3 +151,19 @@ def test_logarithms_of_rows_that_see_a_nan(kernel, monkeypatch):
         _, lse = attend(b, q, 2, sinks=sinks)
         assert np.isnan(want).any() and not np.isnan(want).all()
         assert np.array_equal(np.isnan(lse), np.isnan(want))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("sink", [np.nan, np.inf])
+def test_a_sink_without_a_value_makes_every_row_of_its_head_nan(sink, kernel, monkeypatch):
+    """Rows without a key too (the first 6 and the last sequence's); the other head is as if alone."""
+    monkeypatch.setenv("MXGEMM_ATTENTION_KERNEL", str(kernel))
+    rng = np.random.default_rng(64)
+    b = Batch(rng, [40, 1, 3], [34, 500, 0], 1, 64, 16, False)
+    q = bf16(rng, b.T, 2 * 64)
+    say("case sinks without a value", sink, kernel)
+    O, lse = attend(b, q, 2, sinks=np.array([sink, 0.5]))
+    assert np.isnan(ref.bf16_to_f64(O[:, 0])).all() and np.isnan(lse[:, 0]).all()
+    want = attend(b, q, 2, sinks=np.array([0.5, 0.5]))
+    assert np.array_equal(O[:, 1], want[0][:, 1]) and np.array_equal(lse[:, 1], want[1][:, 1])
+    check(b, q, 2, want, sinks=np.array([0.5, 0.5]))
