@@ -154,7 +154,11 @@ __device__ __forceinline__ int seq_groups(const AttnArgs &a, const AttnSeq &q, i
 // The first key that a token at position p sees (a window may be as long as an
 // int is: p - window alone would wrap below 0, and so would a limit below 0 less
 // the first key of a block)
-__device__ __forceinline__ int first_key(const AttnArgs &a, int p) { return a.window > 0 ? max(p, a.window - 1) - (a.window - 1) : 0; }
+__device__ __forceinline__ int first_key(const AttnArgs &a, int p)
+{
+    const int before = a.window > 0 ? a.window - 1 : 0x7FFFFFFF;  // keys before p that it sees
+    return max(p, before) - before;
+}
 
 // Keys [lo, hi) that the tokens i0 .. i1 of a sequence can see between them
 __device__ __forceinline__ void tile_keys(const AttnArgs &a, const AttnSeq &q, int i0, int i1, int &lo, int &hi)
