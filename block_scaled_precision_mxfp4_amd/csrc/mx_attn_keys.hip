@@ -6,7 +6,8 @@
 // 35 us, 4.8 TB/s.  One token over 4096 (16.8 MB) takes 12 us, mostly one after
 // another: plan and page ids 1.3, first keys, 2 blocks a wave, parts, their sum.
 // 8 x 5 tokens over 16384 in 8 bits, 8 query heads a key head: 36 us, 2.4 TB/s:
-// one wave a SIMD with 64 rows, whose products and exponentials do not overlap.
+// its units are cut into parts, one workgroup a compute unit, so that a SIMD has
+// one wave of 64 rows, whose products and exponentials do not overlap.
 //
 // Each wave has a ring of its own in LDS, filled by direct-to-LDS loads of
 // whole rows (page ids come by LDS as well, a page's descriptor ends with the

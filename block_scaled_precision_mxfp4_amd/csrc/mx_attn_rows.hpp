@@ -10,9 +10,9 @@ namespace mx {
 // Waves of a workgroup, keys of a stage and stages in LDS.  SMALL: half the rows
 // and two workgroups on a compute unit, which fill each other's barriers and ends;
 // the large shape reads keys and values half as often.  A prompt of 8192 tokens,
-// 32 heads of 128 (550 GFLOP of the causal half): 541 us, 1.0 PFLOP/s, where a
-// large bf16 product of the library's reaches 1.2 to 1.3; counters at 550 us: the
-// matrix units busy 46 % of the cycles, the vector units 48 %, LDS 22 %.  On one
+// 32 heads of 128 (550 GFLOP of the causal half): 541 to 634 us by the card, 0.87 to
+// 1.0 PFLOP/s, where a large bf16 product of the library's reaches 1.2 to 1.3;
+// counters: the matrix units busy 48 % of the cycles, the vector units 50 %.  On one
 // SIMD the two overlap only in part (two waves of 32-cycle products with 8 vector
 // instructions to each take 335 us where the products alone take 245 and the
 // vector instructions 175), so that what is left is in the vector instructions of
